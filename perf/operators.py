@@ -451,12 +451,10 @@ def _run_own(s):
         return s["packed"], s["gamma"], s["V"]
     if c["op"] == "attn":
         return api.paged_attn(h["layout"], h["tables"], s["q"], h["cache"], s["table"], s["lens"], cu_q=s["cu"],
-                              max_q=s["max_q"], max_kv=s["max_kv"], causal=c["causal"], dtype=torch.bfloat16,
-                              workspace=h["workspace"])
+                              causal=c["causal"], dtype=torch.bfloat16, workspace=h["workspace"])
     if c["op"] == "mass":
         return api.paged_mass(h["layout"], h["tables"], s["q"], s["lse"], h["cache"], s["table"], s["lens"], s["mass"],
-                              cu_q=s["cu"], max_q=s["max_q"], max_kv=s["max_kv"], causal=c["causal"], decay=0.9,
-                              out=s["new_mass"], workspace=h["workspace"])
+                              cu_q=s["cu"], causal=c["causal"], decay=0.9, out=s["new_mass"], workspace=h["workspace"])
     lens, kept, mass = api.paged_evict(h["layout"], h["cache"], s["table"], s["lens"], s["mass"], c["keep"], s["into"],
                                        sink=c["sink"], recent=c["recent"])
     return {"lens": lens, "kept": kept, "mass": mass, "packed": s["packed"], "gamma": s["gamma"], "V": s["V"]}
