@@ -423,9 +423,11 @@ def _evict_plain(s):
 def _handle(s):
     """What a program makes once and keeps: layout, tables, the cache object over its pools, a workspace."""
     if "handle" not in s:
-        from rotation_preconditioned_quantization_b200 import api
+        import rotation_preconditioned_quantization_b200 as api
 
         c, h = s["case"], {"api": api}
+        if c["op"] == "rope":
+            h["table"] = api.RopeTable(s["sections"], theta=10000.0, per_axis=c["per_axis"])
         if c["op"] != "rope":
             h["layout"] = api.Layout(c["d"], c["b"])
             h["cache"] = api.PagedCache(s["packed"], s["gamma"], s["V"])
@@ -443,8 +445,7 @@ def _run_own(s):
     c, h = s["case"], _handle(s)
     api = h["api"]
     if c["op"] == "rope":
-        out = api.rope(s["q"], s["positions"], s["sections"], k=s["k"], theta=10000.0, interleaved=c["interleaved"],
-                       per_axis=c["per_axis"], inverse=c["inverse"])
+        out = api.rope(s["q"], s["positions"], h["table"], k=s["k"], interleaved=c["interleaved"], inverse=c["inverse"])
         return list(out) if s["k"] is not None else [out]
     if c["op"] == "write":
         api.paged_write(h["layout"], h["staged"], s["new_V"], h["cache"], s["table"], s["starts"], s["cu"])
