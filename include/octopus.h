@@ -302,6 +302,170 @@ OCTO_API int octo_dequant(const octo_layout* L, const octo_tables* tables,
                           const uint32_t* packed, const float* gamma, void* out, int out_dtype,
                           octo_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Paged cache
+ * -----------
+ * The compressed cache of many sequences in a pool of pages of page_size
+ * token slots, each page holding every KV head (word-planar like the
+ * contiguous cache above; a contiguous cache of n_heads = B*Hkv heads is the
+ * pool of B pages of Hkv heads and page_size = cache_cap slots). Slot s of
+ * sequence i lives in page pages[i*stride + s / page_size] at offset
+ * s mod page_size; cache head h uses sign row h mod tables->n_heads. The
+ * layout must be the OCTOPUS split without the sketch (else
+ * OCTO_EUNSUPPORTED).
+ *
+ * Page ids, lengths and offsets are device data that the host does not see.
+ * The kernels never read or write outside the pool and the tables because of
+ * them: they OR bits into *status (when not NULL) and go on, see
+ * octo_paged_status. The outputs of the sequences concerned are then
+ * unspecified. */
+typedef struct octo_pages {
+  uint32_t* packed;  /* [n_pages][n_heads][W][page_size] */
+  float* gamma;      /* [n_pages][n_heads][page_size] */
+  void* V;           /* bf16 [n_pages][n_heads][page_size][d], 16-byte aligned */
+  int64_t n_pages;   /* >= 1 */
+  int32_t n_heads;   /* KV heads */
+  int32_t page_size; /* token slots per page, a multiple of 16 */
+  int32_t* status;   /* device word of octo_paged_status bits, or NULL */
+} octo_pages;
+
+typedef struct octo_page_table {
+  const int32_t* pages; /* device [n_seqs][stride]; entries behind a sequence's last page are not read */
+  int64_t stride;       /* entries between rows, >= max_pages */
+  int32_t n_seqs;
+  int32_t max_pages;    /* entries per row that may be read */
+} octo_page_table;
+
+enum octo_paged_status {
+  OCTO_PAGED_TIMEOUT = 1,   /* a bounded on-chip wait expired: the call's outputs are invalid */
+  OCTO_PAGED_BAD_PAGE = 2,  /* a page id outside [0, n_pages): reads took page 0 instead, writes were dropped */
+  OCTO_PAGED_BAD_LENGTH = 4 /* a length or offset that the tables do not hold (negative, behind the table, not ascending): clamped */
+};
+
+/* Device. Rotary positions with up to four axes on the rows of two tensors
+ * (queries and, optionally, keys: the step before octo_encode). Row t, head
+ * h, frequency i in [0, F), F = the sum of the sections: the pair
+ * (x_i, x_{i+F}) (half-split), or (x_2i, x_2i+1) when interleaved, is turned
+ * by the angle pos[axis(i)][t] * theta^(-e_i); coordinates from 2F on are
+ * copied. The first sections[0] frequencies belong to axis 0, the next
+ * sections[1] to axis 1, and so on. e_i = i / F with one frequency scale over
+ * all axes, or j / sections[axis] for the j-th frequency of its axis
+ * (per_axis). inverse turns back: it is the transpose, so also the gradient
+ * of the forward call. Angles are exact to 2^-32 of a turn at every 32-bit
+ * position.
+ *   x0, y0  device rows [n_tokens][heads0][d] in and out, dtype OCTO_F32 or
+ *           OCTO_BF16, element strides (token, head), the last axis
+ *           contiguous; y may be x, and must not overlap it otherwise.
+ *   x1, y1  the second pair of tensors, heads1 heads (0: none).
+ *   positions device int32 [n_axes][pos_stride].
+ *   freqs   device uint64 [F], from octo_rope_freqs.
+ * Errors: OCTO_EINVAL (NULL pointer, negative size, odd d, 2F > d, bad
+ * dtype, pos_stride < n_tokens), OCTO_EUNSUPPORTED (d > 1024, n_axes outside
+ * 1..4). n_tokens == 0 or no heads launches nothing. */
+typedef struct octo_rope_tensor {
+  const void* x;
+  void* y;
+  int32_t heads;
+  int64_t x_token_stride, x_head_stride, y_token_stride, y_head_stride;
+} octo_rope_tensor;
+OCTO_API int octo_rope(const octo_rope_tensor* a, const octo_rope_tensor* b, int dtype, int64_t n_tokens, int d,
+                       const int32_t* positions, int64_t pos_stride, int n_axes, const int32_t* sections,
+                       const uint64_t* freqs, int interleaved, int inverse, octo_stream_t stream);
+
+/* Host. Frequencies of octo_rope in 2^-64 turns per position (caller-allocated
+ * host array of sum(sections) values): round(theta^(-e_i) / (2 pi) * 2^64).
+ * Errors: OCTO_EINVAL (NULL, a negative section, theta not finite or below
+ * 1), OCTO_EUNSUPPORTED (n_axes outside 1..4). */
+OCTO_API int octo_rope_freqs(double theta, int n_axes, const int32_t* sections, int per_axis, uint64_t* freqs);
+
+/* Device. Writes new tokens into pages: token t of sequence i (packed row
+ * r = cu[i] + t, 0 <= t < cu[i+1] - cu[i]) goes to slot starts[i] + t.
+ *   packed, gamma  the tokens' codes as octo_encode left them in a contiguous
+ *                  staging cache of pages->n_heads heads, capacity
+ *                  staged_cap >= n_rows, rows [0, n_rows).
+ *   V              device bf16, row r of head h at V + r*v_row_stride +
+ *                  h*v_head_stride (elements), d contiguous; pointer and
+ *                  strides multiples of 16 bytes. The pool's V may be NULL
+ *                  with V NULL (keys only).
+ *   starts, cu     device int32 [n_seqs], [n_seqs + 1].
+ * Two tokens must not go to one slot. Errors: OCTO_EINVAL, and
+ * OCTO_EUNSUPPORTED for a layout outside the paged set. n_rows == 0 launches
+ * nothing. */
+OCTO_API int octo_paged_write(const octo_layout* L, const octo_pages* pages, const octo_page_table* table,
+                              const uint32_t* packed, const float* gamma, int64_t staged_cap,
+                              const void* V, int64_t v_row_stride, int64_t v_head_stride, int64_t n_rows,
+                              const int32_t* starts, const int32_t* cu, octo_stream_t stream);
+
+/* Device. Attention of a chunk of new query tokens over a paged cache that
+ * already holds them (octo_paged_write first): packed query rows
+ * cu_q[i] .. cu_q[i+1] - 1 are the last new_i = cu_q[i+1] - cu_q[i] tokens
+ * of sequence i, whose cache holds seq_lens[i] slots. With causal != 0, new
+ * token t sees the slots below seq_lens[i] - new_i + t + 1, else all
+ * seq_lens[i]. Logits are scale * gamma_n * <R q, u_hat_n> as in
+ * octo_decode_attn; a row that sees nothing gives out = 0, lse = -inf.
+ *   q    device, row r head h at q + r*q_row_stride + h*q_head_stride
+ *        (elements), q_dtype OCTO_F32 or OCTO_BF16, d contiguous.
+ *        Query head hq reads KV head hq / (Hq / n_heads).
+ *   out  device [n_rows][Hq][d], out_dtype OCTO_F32 or OCTO_BF16, 16-byte aligned.
+ *   lse  device fp32 [n_rows][Hq] ln sum exp(logits), or NULL.
+ *   workspace  device, 256-byte aligned, octo_paged_attn_workspace() bytes of
+ *        scratch; nothing in it needs to be kept or cleared between calls.
+ *        Calls that share it must not overlap on the GPU.
+ * Keys and queries enter the tensor cores as fp16 (queries scaled by a power
+ * of two per row), weights and V as bf16; sums and softmax statistics are
+ * fp32. Values of slots that a row does not see, but another row of its
+ * sequence does, must be finite. Two launches.
+ * Supported: d in {64, 128}, b in {2, 3, 4}, Hq / n_heads <= 256.
+ * Errors: OCTO_EINVAL, OCTO_EUNSUPPORTED, OCTO_EWORKSPACE. n_rows == 0
+ * launches nothing. */
+OCTO_API size_t octo_paged_attn_workspace(const octo_layout* L, int64_t n_rows, int n_seqs, int Hq, int Hkv);
+OCTO_API int octo_paged_attn(const octo_layout* L, const octo_tables* tables, const octo_pages* pages,
+                             const octo_page_table* table, const int32_t* seq_lens, const void* q, int q_dtype,
+                             int64_t q_row_stride, int64_t q_head_stride, int64_t n_rows, int Hq, const int32_t* cu_q,
+                             int causal, float scale, void* out, int out_dtype, float* lse,
+                             void* workspace, size_t ws_bytes, octo_stream_t stream);
+
+/* Device. The attention weight that each cached token gathers from a chunk
+ * (what eviction by accumulated weight ranks): for every sequence i, cache
+ * head h and slot j < seq_lens[i]
+ *   mass_out[i][h][j] = decay * mass_in[i][h][j]
+ *                       + sum over the chunk's rows and the head's query heads of exp(logit_j - lse)
+ * with the logits, masks and rows of octo_paged_attn and its lse. Slots from
+ * seq_lens[i] on are left as they were. The sums have a fixed order.
+ *   mass_in, mass_out device fp32 [n_seqs][n_heads][mass_stride] (the same
+ *        array, or not overlapping); mass_in NULL reads as 0. Slots at and
+ *        beyond mass_stride are not counted (OCTO_PAGED_BAD_LENGTH).
+ * Logits are formed from fp16 pairs (hi + lo, 22 bits) on the tensor cores.
+ * Two launches. Supported shapes, workspace rules and errors as
+ * octo_paged_attn. */
+OCTO_API size_t octo_paged_mass_workspace(const octo_layout* L, int64_t n_rows, int n_seqs, int Hq, int Hkv);
+OCTO_API int octo_paged_mass(const octo_layout* L, const octo_tables* tables, const octo_pages* pages,
+                             const octo_page_table* table, const int32_t* seq_lens, const void* q, int q_dtype,
+                             int64_t q_row_stride, int64_t q_head_stride, int64_t n_rows, int Hq, const int32_t* cu_q,
+                             int causal, float scale, const float* lse, float decay, const float* mass_in,
+                             float* mass_out, int64_t mass_stride, void* workspace, size_t ws_bytes,
+                             octo_stream_t stream);
+
+/* Device. Cuts sequences back to at most `keep` slots per cache head: of the
+ * n = min(seq_lens[i], mass_stride) slots of each (sequence, head) the first
+ * `sink`, the last `recent` and those of the largest mass between them stay
+ * (ties: the lower slot; NaN ranks below every number), keep in all, or all
+ * n when n <= keep. They keep their order and move to slots 0.. of the
+ * sequence's row in dst_table, in the pool `dst` (which may be `src`; the
+ * pages written must not be read by this call). Two launches.
+ *   mass     device fp32 [n_seqs][n_heads][mass_stride].
+ *   kept     device int32 [n_seqs][n_heads][keep]: the slots kept, ascending; -1 from n on.
+ *   new_lens device int32 [n_seqs]: min(n, keep).
+ *   new_mass device fp32 [n_seqs][n_heads][keep] (0 from n on), or NULL.
+ * Errors: OCTO_EINVAL (NULL pointer, keep < 1, sink or recent < 0, sink +
+ * recent > keep, pools of different heads or page size, one pool with V and
+ * the other without, a destination table shorter than keep), OCTO_EUNSUPPORTED (layout; n_seqs * n_heads
+ * > 65535). n_seqs == 0 launches nothing. */
+OCTO_API int octo_paged_evict(const octo_layout* L, const octo_pages* src, const octo_page_table* src_table,
+                              const int32_t* seq_lens, const float* mass, int64_t mass_stride, int32_t keep,
+                              int32_t sink, int32_t recent, const octo_pages* dst, const octo_page_table* dst_table,
+                              int32_t* kept, int32_t* new_lens, float* new_mass, octo_stream_t stream);
+
 /* Static string for a status code. */
 OCTO_API const char* octo_status_string(int status);
 

@@ -15,6 +15,7 @@ LIB_PATH = os.path.join(_HERE, "liboctopus_b200.so")
 OCTO_OK, OCTO_EINVAL, OCTO_EUNSUPPORTED, OCTO_ECUDA, OCTO_EWORKSPACE = 0, -1, -2, -3, -4
 ROUND_SCALAR, ROUND_JOINT = 0, 1
 F32, BF16 = 0, 1
+PAGED_TIMEOUT, PAGED_BAD_PAGE, PAGED_BAD_LENGTH = 1, 2, 4
 
 
 class OctoLayout(ctypes.Structure):
@@ -27,6 +28,23 @@ class OctoTables(ctypes.Structure):
     _fields_ = [("dir_c", ctypes.c_void_p), ("dir_t", ctypes.c_void_p), ("rho_c", ctypes.c_void_p),
                 ("rho_t", ctypes.c_void_p), ("signs", ctypes.c_void_p), ("qjl_S", ctypes.c_void_p),
                 ("n_heads", ctypes.c_int64)]
+
+
+class OctoPages(ctypes.Structure):
+    _fields_ = [("packed", ctypes.c_void_p), ("gamma", ctypes.c_void_p), ("V", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int64), ("n_heads", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("status", ctypes.c_void_p)]
+
+
+class OctoPageTable(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("stride", ctypes.c_int64), ("n_seqs", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32)]
+
+
+class OctoRopeTensor(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p), ("heads", ctypes.c_int32),
+                ("x_token_stride", ctypes.c_int64), ("x_head_stride", ctypes.c_int64),
+                ("y_token_stride", ctypes.c_int64), ("y_head_stride", ctypes.c_int64)]
 
 
 class OctoError(RuntimeError):
@@ -69,6 +87,34 @@ _SIGS = {
     "octo_dequant": (ctypes.c_int, [ctypes.POINTER(OctoLayout), ctypes.POINTER(OctoTables), ctypes.c_int64, ctypes.c_int64,
                                     ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                     ctypes.c_int, ctypes.c_void_p]),
+    "octo_rope": (ctypes.c_int, [ctypes.POINTER(OctoRopeTensor), ctypes.POINTER(OctoRopeTensor), ctypes.c_int,
+                                 ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int,
+                                 ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int, ctypes.c_int, ctypes.c_void_p]),
+    "octo_rope_freqs": (ctypes.c_int, [ctypes.c_double, ctypes.c_int, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p]),
+    "octo_paged_write": (ctypes.c_int, [ctypes.POINTER(OctoLayout), ctypes.POINTER(OctoPages),
+                                        ctypes.POINTER(OctoPageTable), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
+                                        ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
+                                        ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "octo_paged_attn_workspace": (ctypes.c_size_t, [ctypes.POINTER(OctoLayout), ctypes.c_int64, ctypes.c_int,
+                                                    ctypes.c_int, ctypes.c_int]),
+    "octo_paged_attn": (ctypes.c_int, [ctypes.POINTER(OctoLayout), ctypes.POINTER(OctoTables), ctypes.POINTER(OctoPages),
+                                       ctypes.POINTER(OctoPageTable), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
+                                       ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int, ctypes.c_void_p,
+                                       ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_int, ctypes.c_void_p,
+                                       ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
+    "octo_paged_mass_workspace": (ctypes.c_size_t, [ctypes.POINTER(OctoLayout), ctypes.c_int64, ctypes.c_int,
+                                                    ctypes.c_int, ctypes.c_int]),
+    "octo_paged_mass": (ctypes.c_int, [ctypes.POINTER(OctoLayout), ctypes.POINTER(OctoTables), ctypes.POINTER(OctoPages),
+                                       ctypes.POINTER(OctoPageTable), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int,
+                                       ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int, ctypes.c_void_p,
+                                       ctypes.c_int, ctypes.c_float, ctypes.c_void_p, ctypes.c_float, ctypes.c_void_p,
+                                       ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t,
+                                       ctypes.c_void_p]),
+    "octo_paged_evict": (ctypes.c_int, [ctypes.POINTER(OctoLayout), ctypes.POINTER(OctoPages),
+                                        ctypes.POINTER(OctoPageTable), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
+                                        ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.POINTER(OctoPages),
+                                        ctypes.POINTER(OctoPageTable), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                        ctypes.c_void_p]),
     "octo_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "octo_abi_version": (ctypes.c_int, []),
 }

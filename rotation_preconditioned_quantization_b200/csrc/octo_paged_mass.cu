@@ -1,0 +1,654 @@
+// The attention weight that cached tokens gather from a chunk of new ones:
+// per slot n the sum over the chunk's rows r (token, query head of the group)
+// of exp(s_rn - lse_r), added to a decayed running mass.
+//
+// The lse of each row is known, so nothing runs along the slots: with the key
+// tile as the M side of the product (S^T = K Q^T, a slot per tensor-memory
+// lane) the sum over rows is a thread's own, in a fixed order, and each key
+// is decoded once however many rows there are.
+//
+// The result is an fp32 statistic, so logits need more than the 11 bits of
+// fp16: keys (times 8) and rotated queries (times scale * log2 e, over a power
+// of two per row) are held as fp16 pairs, hi + lo, and S = K_lo Q_hi + K_hi
+// Q_lo + K_hi Q_hi (the dropped product is below 2^-22). The products are
+// what bounds long chunks: three times the one product's time.
+//
+// A first kernel rotates and splits the queries into the tiles the second
+// one's bulk copies bring: 64 rows, hi then lo, already swizzled.
+//
+// Second kernel, per CTA a contiguous run of units of 256 slots of one
+// (sequence, head); cuts follow the units' cost. Warps (18): 0-3 and 4-7 sum
+// the weights of the unit's first and second 128 slots, 8-11 and 12-15 decode
+// them, 16 issues the products, 17 copies query tiles. Both halves use a
+// query tile while it is in shared memory, which halves what the copies move.
+
+#include <algorithm>
+
+#include "octo_paged.cuh"
+
+namespace octo {
+namespace paged {
+
+constexpr int kQRows = 64;    // rows of a query tile
+constexpr int kUnit = 256;    // slots of a unit
+constexpr float kKeyUp = 8.0f;  // keys are held times 8: their low parts stay clear of fp16's subnormals
+constexpr int kQPanel = kQRows * 128, kKPanel = 128 * 128;
+
+struct MassArgs {
+  Table t;
+  const uint32_t* packed;
+  const float* gamma;
+  const float* dir_c;
+  const float* rho_c;
+  const float* signs;
+  int64_t table_heads;
+  const int32_t* seq_lens;
+  const int32_t* cu;
+  const void* q;
+  int64_t q_row, q_head, n_rows;
+  int q_bf16, Hq, g, causal;
+  float scale, decay;
+  const float* lse;
+  const float* mass_in;
+  float* mass_out;
+  int64_t mass_stride, n_tiles;  // n_tiles: row tiles that the workspace holds per head
+  unsigned char* tiles;  // [row tile][head][hi, lo] images
+  float4* rows;          // [row tile][head][64]: 2^e, lse * log2 e, its rounding's factor, slots seen (as int)
+};
+
+__device__ __forceinline__ int query_tiles(const Seq& s, int g) { return (s.fresh * g + kQRows - 1) / kQRows; }
+
+__device__ __forceinline__ int64_t scan64(int64_t v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+
+// ---- queries: rotate, scale, split ---------------------------------------------
+template <int D>
+__global__ void __launch_bounds__(256) paged_mass_prep(const __grid_constant__ MassArgs a) {
+  constexpr int E = D / 32, NP = D / 64;
+  const int h = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __shared__ int s_i, s_m;
+  if (warp == 0) {
+    int64_t before = 0;
+    bool found = false;
+    for (int base = 0; base < a.t.n_seqs; base += 32) {
+      const int i = base + lane;
+      const int mt = i < a.t.n_seqs ? query_tiles(seq_of(a.t, a.seq_lens, a.cu, a.n_rows, i, blockIdx.x == 0 && h == 0), a.g) : 0;
+      const int64_t end = before + scan64(mt, lane);
+      if (static_cast<int64_t>(blockIdx.x) < end && static_cast<int64_t>(blockIdx.x) >= end - mt) {
+        s_i = i;
+        s_m = static_cast<int>(blockIdx.x - (end - mt));
+        found = true;
+      }
+      before = __shfl_sync(0xffffffffu, end, 31);
+    }
+    if (!__any_sync(0xffffffffu, found) && lane == 0) s_i = -1;
+  }
+  __syncthreads();
+  const int i = s_i, m = s_m;
+  if (i < 0) return;
+  const Seq s = seq_of(a.t, a.seq_lens, a.cu, a.n_rows, i);
+  const int rows = min(kQRows, s.fresh * a.g - m * kQRows), padded = (rows + 15) / 16 * 16;
+  const int64_t tile = static_cast<int64_t>(blockIdx.x) * a.t.n_heads + h;
+  unsigned char* hi = a.tiles + tile * (2 * NP * kQPanel);
+  unsigned char* lo = hi + NP * kQPanel;
+  float4* info = a.rows + tile * kQRows;
+  const float* sg = a.signs + (h % a.table_heads) * D + lane * E;
+  // 1 / sqrt(d) of the rotation, the softmax scale and log2 e in one factor
+  const float pre = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634 / sqrt(static_cast<double>(D)));
+  for (int r = warp; r < padded; r += 8) {
+    const bool there = r < rows;
+    const int rr = m * kQRows + r, tok = rr / a.g, hq = h * a.g + rr % a.g;
+    float v[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = 0.0f;
+    if (there) {
+      const int64_t off = (s.row0 + tok) * a.q_row + hq * a.q_head + lane * E;
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        v[e] = sg[e] * (a.q_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[off + e])
+                                 : static_cast<const float*>(a.q)[off + e]);
+    }
+    fwht_warp<E>(v, lane);
+    float mx = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+      v[e] *= pre;
+      mx = fmaxf(mx, fabsf(v[e]));
+    }
+    mx = warp_max(mx);
+    const int ex = min(max(static_cast<int>(__float_as_uint(mx) >> 23) - 126, -120), 120);  // 2^ex > mx
+    const float down = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+    unsigned char *ph = hi + sw128(r, lane * E / 8, kQPanel) + (lane * E % 8) * 2, *pl = ph + (lo - hi);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+      const float x = v[e] * down, y = v[e + 1] * down;
+      const __half2 t = __floats2half2_rn(x, y);
+      const float2 b = __half22float2(t);
+      *reinterpret_cast<uint32_t*>(ph + 2 * e) = *reinterpret_cast<const uint32_t*>(&t);
+      *reinterpret_cast<uint32_t*>(pl + 2 * e) = half2_bits(x - b.x, y - b.y);
+    }
+    if (lane == 0) {
+      float4 f = make_float4(0.0f, INFINITY, 0.0f, __int_as_float(0));
+      if (there) {
+        const float l = a.lse[static_cast<int64_t>(s.row0 + tok) * a.Hq + hq];
+        const double l2 = static_cast<double>(l) * 1.4426950408889634;
+        const float up = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23) / kKeyUp;
+        const int seen = a.causal ? max(0, s.len - s.fresh + tok + 1) : s.len;
+        if (l == -INFINITY)  // a row that saw nothing gives nothing
+          f = make_float4(up, INFINITY, 0.0f, __int_as_float(0));
+        else
+          f = make_float4(up, static_cast<float>(l2),
+                          exp2f(static_cast<float>(static_cast<double>(static_cast<float>(l2)) - l2)), __int_as_float(seen));
+        if (!(fabsf(l) < INFINITY) && l != -INFINITY) f.z = 1.0f;  // +inf: weight 0; NaN stays
+      }
+      info[r] = f;
+    }
+  }
+}
+
+// ---- units ----------------------------------------------------------------------
+__device__ __forceinline__ int64_t unit_cost(const Seq& s, int g) { return 4 + 6 * static_cast<int64_t>(query_tiles(s, g)); }
+__device__ __forceinline__ int units_of(const Seq& s) { return (s.len + kUnit - 1) / kUnit; }
+
+struct UnitPlace {
+  int64_t count;  // units of this CTA
+  int64_t tile0;  // query tiles of the sequences before i
+  int i, h, u;
+};
+
+// Walks a CTA's units.
+struct Units {
+  const MassArgs& a;
+  int64_t left, tile0;
+  int i, h, u, first, tiles;  // query tiles [first, tiles) see a slot of the unit
+  Seq s;
+  __device__ Units(const MassArgs& a_, const UnitPlace& p) : a(a_), left(p.count), tile0(p.tile0), i(p.i), h(p.h), u(p.u) {
+    if (left > 0) {
+      s = seq_of(a.t, a.seq_lens, a.cu, a.n_rows, i);
+      open();
+    }
+  }
+  __device__ void open() {
+    tiles = static_cast<int>(min(static_cast<int64_t>(query_tiles(s, a.g)), max(static_cast<int64_t>(0), a.n_tiles - tile0)));
+    first = 0;
+    // rows before token u*256 - (len - fresh) see no slot of the unit
+    if (a.causal) first = static_cast<int>(min(static_cast<int64_t>(tiles), static_cast<int64_t>(max(0, u * kUnit - s.len + s.fresh)) * a.g / kQRows));
+  }
+  __device__ bool on() const { return left > 0; }
+  __device__ int cols(int m) const { return min(kQRows, (s.fresh * a.g - m * kQRows + 15) / 16 * 16); }
+  __device__ void next() {
+    if (--left <= 0) return;
+    if (++u >= units_of(s)) {
+      u = 0;
+      if (++h >= a.t.n_heads) {
+        h = 0;
+        do {
+          tile0 += query_tiles(s, a.g);
+          ++i;
+          s = seq_of(a.t, a.seq_lens, a.cu, a.n_rows, i);
+        } while (s.len <= 0);
+      }
+    }
+    open();
+  }
+};
+
+// CTA b takes the units whose cost prefix falls into [b, b + 1) / ctas of the
+// whole cost; warp-wide.
+__device__ UnitPlace find_units(const MassArgs& a, int lane) {
+  int64_t total = 0;
+  for (int i = lane; i < a.t.n_seqs; i += 32) {
+    const Seq s = seq_of(a.t, a.seq_lens, a.cu, a.n_rows, i);
+    total += unit_cost(s, a.g) * units_of(s) * a.t.n_heads;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  const int64_t w0 = blockIdx.x * total / gridDim.x, w1 = (blockIdx.x + 1) * total / gridDim.x;
+  UnitPlace p{0, 0, -1, 0, 0};
+  int64_t before = 0, tiles = 0;
+  for (int base = 0; base < a.t.n_seqs; base += 32) {
+    const int i = base + lane;
+    Seq s{0, 0, 0};
+    if (i < a.t.n_seqs) s = seq_of(a.t, a.seq_lens, a.cu, a.n_rows, i);
+    const int64_t n = static_cast<int64_t>(units_of(s)) * a.t.n_heads, c = unit_cost(s, a.g), w = n * c;
+    const int64_t end = before + scan64(w, lane), start = end - w;
+    const int64_t tend = tiles + scan64(query_tiles(s, a.g), lane);
+    // units k of this sequence with start + k * c in [w0, w1)
+    const int64_t k0 = min(n, max(static_cast<int64_t>(0), (w0 - start + c - 1) / c)),
+                  k1 = min(n, max(static_cast<int64_t>(0), (w1 - start + c - 1) / c));
+    int64_t mine = (start >= w1 || end <= w0) ? 0 : k1 - (w0 <= start ? 0 : k0);
+    mine = max(mine, static_cast<int64_t>(0));
+    const uint32_t has = __ballot_sync(0xffffffffu, mine > 0);
+    if (has && p.i < 0) {
+      const int who = __ffs(has) - 1;
+      const int64_t k = w0 <= start ? 0 : k0;
+      const int uo = units_of(s);
+      p.i = __shfl_sync(0xffffffffu, i, who);
+      p.h = __shfl_sync(0xffffffffu, uo ? static_cast<int>(k / uo) : 0, who);
+      p.u = __shfl_sync(0xffffffffu, uo ? static_cast<int>(k % uo) : 0, who);
+      p.tile0 = __shfl_sync(0xffffffffu, tend - query_tiles(s, a.g), who);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    p.count += mine;
+    before = __shfl_sync(0xffffffffu, end, 31);
+    tiles = __shfl_sync(0xffffffffu, tend, 31);
+  }
+  return p;
+}
+
+template <int D, int B>
+struct MassCfg {
+  using K = Code<D, B>;
+  static constexpr int NP = D / 64;
+  static constexpr int KT = NP * kKPanel;          // one part (hi or lo) of a 128-slot key tile
+  static constexpr int QT = NP * kQPanel;          // one part of a query tile
+  // b <= 3: every signed code as {x, y hi | z hi | x, y lo | z lo} (fp16
+  // pairs), 16 bytes; b = 4: the unit directions in fp32, times the norm
+  // level in registers (8192 codes would need 128 KB).
+  static constexpr bool SPLIT = B == 4;
+  static constexpr int NE = SPLIT ? K::NDIR : 1 << K::C;
+  static constexpr int REP = NE <= 128 ? 8 : 1;
+  static constexpr int SH = 4 + (REP == 8 ? 3 : 0);
+  static constexpr int KB = 0, QB = 4 * KT, TAB = QB + 4 * QT, RHO = TAB + (NE << SH), ROWS = RHO + 32;
+  static constexpr int BARS = ROWS + 2 * kQRows * 16, PLACE = BARS + 16 * 8, TMEM = PLACE + 40, DIR = PLACE + 48,
+                       SMEM = DIR + 128;
+  static constexpr int THREADS = 576;
+  static_assert(SMEM <= 232448, "shared memory of an SM");
+};
+
+enum { mKF = 0, mKE = 2, mQF = 4, mQE = 6, mDF = 8, mDE = 12 };  // D barriers: [half][buffer]; the sixteen fill 128 bytes
+
+template <int D, int B>
+__device__ __forceinline__ bool mass_decode(const MassArgs& a, const UnitPlace& place, unsigned char* sm, uint32_t base,
+                                            uint32_t bars, int half) {
+  using Cfg = MassCfg<D, B>;
+  using K = Code<D, B>;
+  constexpr int W = K::W, T = K::T;
+  const int n = threadIdx.x & 127, lane = threadIdx.x & 31;
+  const uint32_t tab = base + Cfg::TAB + (lane & (Cfg::REP - 1)) * 16;
+  const float* rho = reinterpret_cast<const float*>(sm + Cfg::RHO);
+  uint32_t w[W];
+  auto fetch = [&](const Units& it) {
+    const int slot = it.u * kUnit + half * 128 + n;
+#pragma unroll
+    for (int k = 0; k < W; ++k) w[k] = 0u;
+    if (slot < it.s.len) {
+      const int pg = max(0, page_of(a.t, it.i, slot));
+      const uint32_t* p = a.packed + (static_cast<int64_t>(pg) * a.t.n_heads + it.h) * W * a.t.page_size + slot % a.t.page_size;
+#pragma unroll
+      for (int k = 0; k < W; ++k) w[k] = __ldg(p + static_cast<int64_t>(k) * a.t.page_size);
+    }
+  };
+  Units it(a, place);
+  while (it.on() && it.first >= it.tiles) it.next();
+  if (it.on()) fetch(it);
+  for (int c = 0; it.on(); ++c) {
+    if (!bar_wait(bars + 8 * (mKE + half), (c & 1) ^ 1)) return false;
+    unsigned char* hi = sm + Cfg::KB + half * 2 * Cfg::KT;
+    unsigned char* lo = hi + Cfg::KT;
+#pragma unroll
+    for (int g0 = 0; g0 < T; g0 += 8) {
+      uint32_t oh[12], ol[12];
+#pragma unroll
+      for (int pr = 0; pr < 4; ++pr) {
+        uint4 e[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int i = g0 + 2 * pr + u;
+          e[u] = make_uint4(0u, 0u, 0u, 0u);
+          if (i < T) {
+            if constexpr (Cfg::SPLIT) {
+              const uint32_t code = code_at<K::C, 0>(w, i);
+              float4 d;
+              asm("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                  : "=f"(d.x), "=f"(d.y), "=f"(d.z), "=f"(d.w)
+                  : "r"(tab + ((code & (K::NDIR - 1)) << Cfg::SH)));
+              const float r = rho[code >> K::DIR];
+              const float x = d.x * r, y = d.y * r, z = d.z * r;
+              const __half2 xy = __floats2half2_rn(x, y), zz = __floats2half2_rn(z, 0.0f);
+              const float2 bx = __half22float2(xy), bz = __half22float2(zz);
+              e[u] = make_uint4(*reinterpret_cast<const uint32_t*>(&xy), *reinterpret_cast<const uint32_t*>(&zz),
+                                half2_bits(x - bx.x, y - bx.y), half2_bits(z - bz.x, 0.0f));
+            } else {
+              asm("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                  : "=r"(e[u].x), "=r"(e[u].y), "=r"(e[u].z), "=r"(e[u].w)
+                  : "r"(tab + code_at<K::C, Cfg::SH>(w, i)));
+            }
+          }
+        }
+        oh[3 * pr] = e[0].x;
+        oh[3 * pr + 1] = lolo(e[0].y, e[1].x);
+        oh[3 * pr + 2] = hilo(e[1].x, e[1].y);
+        ol[3 * pr] = e[0].z;
+        ol[3 * pr + 1] = lolo(e[0].w, e[1].z);
+        ol[3 * pr + 2] = hilo(e[1].z, e[1].w);
+      }
+#pragma unroll
+      for (int q = 0; q < 3; ++q) {
+        const int chunk = g0 / 8 * 3 + q;
+        if (chunk < D / 8) {
+          const uint32_t at = sw128(n, chunk, kKPanel);
+          *reinterpret_cast<uint4*>(hi + at) = make_uint4(oh[4 * q], oh[4 * q + 1], oh[4 * q + 2], oh[4 * q + 3]);
+          *reinterpret_cast<uint4*>(lo + at) = make_uint4(ol[4 * q], ol[4 * q + 1], ol[4 * q + 2], ol[4 * q + 3]);
+        }
+      }
+    }
+    fence_async_shared();
+    bar_arrive(bars + 8 * (mKF + half));
+    do it.next();
+    while (it.on() && it.first >= it.tiles);
+    if (it.on()) fetch(it);
+  }
+  return true;
+}
+
+template <int D, int B>
+__device__ __forceinline__ bool mass_copies(const MassArgs& a, const UnitPlace& place, uint32_t base, uint32_t bars,
+                                            int& issued) {
+  using Cfg = MassCfg<D, B>;
+  const int lane = threadIdx.x & 31;
+  int c = 0;
+  for (Units it(a, place); it.on(); it.next())
+    for (int m = it.first; m < it.tiles; ++m, ++c) {
+      const int st = c & 1;
+      if (!bar_wait(bars + 8 * (mQE + st), ((c >> 1) & 1) ^ 1)) return false;
+      const uint32_t n = it.cols(m), bytes = n * 128;
+      const int64_t tile = (it.tile0 + m) * a.t.n_heads + it.h;
+      const unsigned char* src = a.tiles + tile * (2 * Cfg::QT);
+      if (lane == 0) {
+        bar_expect(bars + 8 * (mQF + st), 2 * Cfg::NP * bytes + n * 16);
+        issued = c + 1;
+        for (int p = 0; p < 2 * Cfg::NP; ++p)
+          bulk_in(base + Cfg::QB + st * 2 * Cfg::QT + p * kQPanel, src + p * kQPanel, bytes, bars + 8 * (mQF + st));
+        bulk_in(base + Cfg::ROWS + st * kQRows * 16, a.rows + tile * kQRows, n * 16, bars + 8 * (mQF + st));
+      }
+      __syncwarp();
+    }
+  return true;
+}
+
+template <int D, int B>
+__device__ __forceinline__ bool mass_products(const MassArgs& a, const UnitPlace& place, uint32_t base, uint32_t bars,
+                                              uint32_t tmem) {
+  using Cfg = MassCfg<D, B>;
+  const bool one = (threadIdx.x & 31) == 0;
+  int c = 0, k = 0;
+  for (Units it(a, place); it.on(); it.next()) {
+    if (it.first >= it.tiles) continue;
+    for (int m = it.first; m < it.tiles; ++m, ++c) {
+      const int st = c & 1;
+      if (!bar_wait(bars + 8 * (mQF + st), (c >> 1) & 1)) return false;
+      const uint32_t idesc = instr_desc(128, it.cols(m), false, false);
+      for (int half = 0; half < 2; ++half) {
+        if (m == it.first && !bar_wait(bars + 8 * (mKF + half), k & 1)) return false;
+        if (!bar_wait(bars + 8 * (mDE + half * 2 + st), ((c >> 1) & 1) ^ 1)) return false;
+        tc_after();
+        if (one) {
+          const uint32_t d = tmem + (half * 2 + st) * kQRows;
+          const uint32_t kh = base + Cfg::KB + half * 2 * Cfg::KT, qh = base + Cfg::QB + st * 2 * Cfg::QT;
+          // small products first
+#pragma unroll
+          for (int part = 0; part < 3; ++part) {
+            const uint32_t ka = part == 0 ? kh + Cfg::KT : kh, qa = part == 1 ? qh + Cfg::QT : qh;
+#pragma unroll
+            for (int s = 0; s < D / 16; ++s)
+              mma_ss(d, smem_desc(ka + (s >> 2) * kKPanel + (s & 3) * 32, 16),
+                     smem_desc(qa + (s >> 2) * kQPanel + (s & 3) * 32, 16), idesc, part + s > 0);
+          }
+          tc_commit(bars + 8 * (mDF + half * 2 + st));
+          if (m + 1 == it.tiles) tc_commit(bars + 8 * (mKE + half));
+          if (half == 1) tc_commit(bars + 8 * (mQE + st));
+        }
+        __syncwarp();
+      }
+    }
+    ++k;
+  }
+  return true;
+}
+
+template <int D, int B>
+__device__ __forceinline__ bool mass_sums(const MassArgs& a, const UnitPlace& place, unsigned char* sm, uint32_t bars,
+                                          uint32_t tmem, int half) {
+  using Cfg = MassCfg<D, B>;
+  const int n = threadIdx.x & 127;
+  const uint32_t D0 = tmem + (static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21) + half * 2 * kQRows;
+  int c = 0;
+  for (Units it(a, place); it.on(); it.next()) {
+    const int slot = it.u * kUnit + half * 128 + n, k0 = slot - n;
+    const bool held = slot < it.s.len, kept = held && slot < a.mass_stride;
+    const int64_t at = (static_cast<int64_t>(it.i) * a.t.n_heads + it.h) * a.mass_stride + slot;
+    float gamma = 0.0f, mass = 0.0f;
+    if (held) {
+      const int pg = max(0, page_of(a.t, it.i, slot));
+      gamma = __ldg(a.gamma + (static_cast<int64_t>(pg) * a.t.n_heads + it.h) * a.t.page_size + slot % a.t.page_size);
+    }
+    if (kept && a.mass_in) mass = a.decay * a.mass_in[at];
+    if (held && !kept) report(a.t.status, OCTO_PAGED_BAD_LENGTH);
+    float sum = 0.0f;
+    for (int m = it.first; m < it.tiles; ++m, ++c) {
+      const int st = c & 1;
+      // the rows' numbers came with the query tile
+      if (!bar_wait(bars + 8 * (mDF + half * 2 + st), (c >> 1) & 1)) return false;
+      if (!bar_wait(bars + 8 * (mQF + st), (c >> 1) & 1)) return false;
+      tc_after();
+      const float4* rows = reinterpret_cast<const float4*>(sm + Cfg::ROWS) + st * kQRows;
+      const int cols = it.cols(m);
+      // some row of the tile does not see some slot of this half, or the half runs past the sequence
+      const bool masked = __float_as_int(rows[0].w) < k0 + 128;
+      float part[2] = {0.0f, 0.0f};
+#pragma unroll 1
+      for (int x0 = 0; x0 < cols; x0 += 16) {
+        uint32_t s[16];
+        tmem_ld16(s, D0 + st * kQRows + x0);
+        tc_wait_ld();
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+          const float4 r = rows[x0 + x];
+          float w = ex2(fmaf(__uint_as_float(s[x]), gamma * r.x, -r.y));
+          if (masked && slot >= __float_as_int(r.w)) w = 0.0f;
+          part[x & 1] = fmaf(w, r.z, part[x & 1]);
+        }
+      }
+      sum += part[0] + part[1];
+      tc_before();
+      bar_arrive(bars + 8 * (mDE + half * 2 + st));
+      bar_arrive(bars + 8 * (mQE + st));
+    }
+    if (kept) a.mass_out[at] = mass + sum;
+  }
+  return true;
+}
+
+template <int D, int B>
+__global__ void __launch_bounds__(576, 1) paged_mass_kernel(const __grid_constant__ MassArgs a) {
+  using Cfg = MassCfg<D, B>;
+  using K = Code<D, B>;
+  extern __shared__ __align__(1024) unsigned char sm[];
+  const uint32_t base = s32(sm), bars = base + Cfg::BARS;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  UnitPlace& s_place = *reinterpret_cast<UnitPlace*>(sm + Cfg::PLACE);
+  uint32_t& s_tmem = *reinterpret_cast<uint32_t*>(sm + Cfg::TMEM);
+  float* s_dir = reinterpret_cast<float*>(sm + Cfg::DIR);
+  float* s_rho = reinterpret_cast<float*>(sm + Cfg::RHO);
+  if (tid < (1 << (B + 1))) s_dir[tid] = a.dir_c[tid];
+  if (tid < K::NRHO) s_rho[tid] = a.rho_c[tid] * kKeyUp;
+  if (warp == 17) {
+    const UnitPlace p = find_units(a, lane);
+    if (lane == 0) s_place = p;
+  }
+  if (tid == 0) {
+    for (int q = 0; q < 2; ++q) {
+      bar_init(bars + 8 * (mKF + q), 128);
+      bar_init(bars + 8 * (mKE + q), 1);
+      bar_init(bars + 8 * (mQF + q), 1);
+      bar_init(bars + 8 * (mQE + q), 1 + 256);
+    }
+    for (int q = 0; q < 4; ++q) {
+      bar_init(bars + 8 * (mDF + q), 1);
+      bar_init(bars + 8 * (mDE + q), 128);
+    }
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 16) tmem_alloc(s32(&s_tmem), 256);
+  __syncthreads();
+  const UnitPlace place = s_place;
+  if (place.count > 0) {
+    for (int e = tid; e < Cfg::NE; e += Cfg::THREADS) {
+      const float3 d = field_direction<B>(e & (K::NDIR - 1), s_dir);
+      uint4 v;
+      if constexpr (Cfg::SPLIT) {
+        v = make_uint4(__float_as_uint(d.x), __float_as_uint(d.y), __float_as_uint(d.z), 0u);
+      } else {
+        const float r = s_rho[e >> K::DIR], x = d.x * r, y = d.y * r, z = d.z * r;
+        const __half2 xy = __floats2half2_rn(x, y), zz = __floats2half2_rn(z, 0.0f);
+        const float2 bx = __half22float2(xy), bz = __half22float2(zz);
+        v = make_uint4(*reinterpret_cast<const uint32_t*>(&xy), *reinterpret_cast<const uint32_t*>(&zz),
+                       half2_bits(x - bx.x, y - bx.y), half2_bits(z - bz.x, 0.0f));
+      }
+#pragma unroll
+      for (int k = 0; k < Cfg::REP; ++k) *reinterpret_cast<uint4*>(sm + Cfg::TAB + (e << Cfg::SH) + k * 16) = v;
+    }
+  }
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = s_tmem;
+  bool ok = true;
+  if (place.count > 0) {
+    if (warp < 8) {
+      ok = mass_sums<D, B>(a, place, sm, bars, tmem, warp >> 2);
+    } else if (warp < 16) {
+      ok = mass_decode<D, B>(a, place, sm, base, bars, (warp - 8) >> 2);
+    } else if (warp == 16) {
+      ok = mass_products<D, B>(a, place, base, bars, tmem);
+      if (!ok) {  // products in flight end before tensor memory is given back (a fresh barrier in the table's place)
+        if (lane == 0) {
+          bar_init(base + Cfg::PLACE, 1);
+          asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+          tc_commit(base + Cfg::PLACE);
+        }
+        __syncwarp();
+        bar_wait(base + Cfg::PLACE, 0);
+      }
+    } else {
+      int issued = 0;
+      ok = mass_copies<D, B>(a, place, base, bars, issued);
+      issued = __shfl_sync(0xffffffffu, issued, 0);
+      // copies in flight end before the CTA does
+      for (int c = max(0, issued - 2); c < issued; ++c) bar_wait(bars + 8 * (mQF + (c & 1)), (c >> 1) & 1);
+    }
+  }
+  if (!ok && lane == 0) report(a.t.status, OCTO_PAGED_TIMEOUT);
+  tc_before();
+  __syncthreads();
+  if (warp == 16) tmem_free(tmem, 256);
+}
+
+// ---- host -------------------------------------------------------------------------
+static int mass_sms() {
+  static std::atomic<int> known[kLaunchCacheDevices];
+  int dev = 0, sms = 148;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+  const bool cached = dev >= 0 && dev < kLaunchCacheDevices;
+  if (cached && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 148;
+  if (cached) known[dev].store(sms, std::memory_order_relaxed);
+  return sms;
+}
+
+// row tiles of all sequences, at most
+static int64_t most_tiles(int64_t n_rows, int n_seqs, int g) { return n_rows * g / kQRows + n_seqs; }
+
+template <int D, int B>
+static cudaError_t launch_mass(const MassArgs& a, cudaStream_t st) {
+  const dim3 grid(static_cast<unsigned>(a.n_tiles), a.t.n_heads);
+  paged_mass_prep<D><<<grid, 256, 0, st>>>(a);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  static LaunchCache cache;
+  int resident = 0;
+  e = launch_setup(paged_mass_kernel<D, B>, cache, MassCfg<D, B>::THREADS, MassCfg<D, B>::SMEM, resident);
+  if (e != cudaSuccess) return e;
+  paged_mass_kernel<D, B><<<mass_sms(), MassCfg<D, B>::THREADS, MassCfg<D, B>::SMEM, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace paged
+}  // namespace octo
+
+extern "C" size_t octo_paged_mass_workspace(const octo_layout* L, int64_t n_rows, int n_seqs, int Hq, int Hkv) {
+  using namespace octo::paged;
+  if (check_layout(L) != OCTO_OK || L->d > 128 || n_rows < 0 || n_seqs < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0)
+    return 0;
+  const size_t tiles = static_cast<size_t>(most_tiles(n_rows, n_seqs, Hq / Hkv)) * Hkv;
+  return 256 + tiles * (static_cast<size_t>(2) * kQRows * L->d * 2 + kQRows * sizeof(float4));
+}
+
+extern "C" int octo_paged_mass(const octo_layout* L, const octo_tables* tab, const octo_pages* pages,
+                               const octo_page_table* table, const int32_t* seq_lens, const void* q, int q_dtype,
+                               int64_t q_row_stride, int64_t q_head_stride, int64_t n_rows, int Hq,
+                               const int32_t* cu_q, int causal, float scale, const float* lse, float decay,
+                               const float* mass_in, float* mass_out, int64_t mass_stride, void* workspace,
+                               size_t ws_bytes, octo_stream_t stream) {
+  using namespace octo::paged;
+  int c = check_layout(L);
+  if (c != OCTO_OK) return c;
+  if (L->d > 128) return OCTO_EUNSUPPORTED;
+  if ((c = check_pages(pages)) != OCTO_OK) return c;
+  if ((c = check_table(table, pages->page_size)) != OCTO_OK) return c;
+  if (!tab || !tab->dir_c || !tab->rho_c || !tab->signs || tab->n_heads < 1) return OCTO_EINVAL;
+  if (q_dtype != OCTO_F32 && q_dtype != OCTO_BF16) return OCTO_EINVAL;
+  if (n_rows < 0 || q_row_stride < 0 || q_head_stride < 0 || Hq < pages->n_heads || Hq % pages->n_heads != 0 ||
+      mass_stride < 0)
+    return OCTO_EINVAL;
+  if (!(scale - scale == 0.0f) || !(decay - decay == 0.0f)) return OCTO_EINVAL;  // NaN or infinite
+  const int g = Hq / pages->n_heads;
+  if (g > 256 || n_rows * g > INT32_MAX - 1024 || pages->n_heads > 65535) return OCTO_EUNSUPPORTED;
+  if (n_rows == 0 || table->n_seqs == 0) return OCTO_OK;
+  if (!q || !lse || !mass_out || !seq_lens || !cu_q) return OCTO_EINVAL;
+  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return OCTO_EINVAL;
+  if (ws_bytes < octo_paged_mass_workspace(L, n_rows, table->n_seqs, Hq, pages->n_heads)) return OCTO_EWORKSPACE;
+  MassArgs a{};
+  a.t = make_table(pages, table);
+  a.packed = pages->packed;
+  a.gamma = pages->gamma;
+  a.dir_c = tab->dir_c;
+  a.rho_c = tab->rho_c;
+  a.signs = tab->signs;
+  a.table_heads = tab->n_heads;
+  a.seq_lens = seq_lens;
+  a.cu = cu_q;
+  a.q = q;
+  a.q_row = q_row_stride;
+  a.q_head = q_head_stride;
+  a.n_rows = n_rows;
+  a.q_bf16 = q_dtype == OCTO_BF16;
+  a.Hq = Hq;
+  a.g = g;
+  a.causal = causal != 0;
+  a.scale = scale;
+  a.decay = decay;
+  a.lse = lse;
+  a.mass_in = mass_in;
+  a.mass_out = mass_out;
+  a.mass_stride = mass_stride;
+  a.n_tiles = most_tiles(n_rows, table->n_seqs, g);
+  const size_t tiles = static_cast<size_t>(a.n_tiles) * pages->n_heads;
+  a.tiles = static_cast<unsigned char*>(workspace);
+  a.rows = reinterpret_cast<float4*>(a.tiles + tiles * (static_cast<size_t>(2) * kQRows * L->d * 2));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (L->d == 64)
+    e = L->b == 2 ? launch_mass<64, 2>(a, st) : L->b == 3 ? launch_mass<64, 3>(a, st) : launch_mass<64, 4>(a, st);
+  else
+    e = L->b == 2 ? launch_mass<128, 2>(a, st) : L->b == 3 ? launch_mass<128, 3>(a, st) : launch_mass<128, 4>(a, st);
+  return e == cudaSuccess ? OCTO_OK : OCTO_ECUDA;
+}
