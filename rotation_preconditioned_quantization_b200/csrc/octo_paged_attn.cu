@@ -5,10 +5,10 @@
 //   s_rn = scale * gamma_n * <R q_r, u_hat_n>,
 // and its output softmax(s_r) V, by one pass over the slots with a running
 // reference m_r and sum l_r (base 2): o_r accumulates 2^(s - m) v, and is
-// rescaled when a logit passes the reference by more than 16 (base 2).
+// rescaled when the weights outgrow the reference (Row below).
 //
 // Matrix work on tcgen05: S = Q K^T with 128-row query tiles (fp16, scaled by
-// a power of two per row so that every |q| <= 1) and 128-slot key tiles, whose
+// a power of two where a row leaves its range) and 128-slot key tiles, whose
 // rows are the decoded unit directions in fp16 (gamma is applied to S in
 // fp32, so a key's norm costs no precision); O += P V with P in bf16 in
 // tensor memory, in place of its S, and V (bf16) as TMA brings it. A CTA
@@ -19,6 +19,14 @@
 // row: no shuffles), and before it the rotation of their queries; 8-11 decode
 // key tiles, a thread per slot, one ahead of the products; 12 issues the
 // products; 13 copies V.
+//
+// Items of at most 128 rows would leave the second query tile empty and the
+// softmax of few rows to few warps. There both S and O pairs serve the one
+// query tile, key tiles alternating between them (so a product runs while the
+// other tile's softmax does), and with at most 64 or 32 rows the query tile
+// holds the rows two or four times, each copy taking its half or quarter of
+// the key tile's columns (weights 0 elsewhere). The copies are rows of their
+// own, with references and sums of their own, and are added at the end.
 //
 // Schedule: the (sequence, head, 256-row tile) items' key tiles form one
 // list, cut into equal contiguous pieces, one per CTA, whatever the lengths.
@@ -40,7 +48,6 @@ namespace paged {
 constexpr int kRows = 256;   // query rows of an item
 constexpr int kKeys = 128;   // slots of a key tile
 constexpr int kPanel = 128 * 128;  // bytes of a 128-row panel of 64 halves
-constexpr float kRaise = 16.0f;    // log2 excess over the reference that raises it: weights stay below 2^16
 
 struct AttnArgs {
   Table t;
@@ -54,12 +61,13 @@ struct AttnArgs {
   const int32_t* cu;
   const void* q;
   int64_t q_row, q_head, n_rows;
-  int q_bf16, Hq, g, causal, box;  // box: V rows per copy
+  int q_bf16, q_vec, Hq, g, causal, box;  // q_vec: a lane's D / 32 query values are one aligned access; box: V rows per copy
   float scale;
   void* out;
   int out_bf16;
   float* lse;
   float* part_o;   // [slots][slot_rows][D]
+  float* copies;   // [CTAs][256][D]: the row copies of an item of at most 128 rows, on their way to their sum
   float2* part_ml; // [slots][slot_rows]
   int slot_rows;
 };
@@ -170,6 +178,11 @@ struct Walk {
   // tiles that hold slots: none for an item whose rows see nothing
   __device__ int work() const { return limit > 0 ? t1 - t0 : 0; }
   __device__ int rows() const { return min(kRows, s.fresh * a.g - m * kRows); }
+  // copies of the rows in a query tile; 0: more than 128 rows, two query tiles
+  __device__ int reps() const {
+    const int r = rows();
+    return r > 128 ? 0 : r > 64 ? 1 : r > 32 ? 2 : 4;
+  }
   __device__ void next() {
     left -= t1 - t0;
     if (left <= 0) return;
@@ -193,17 +206,19 @@ struct AttnCfg {
   using K = Code<D, B>;
   static constexpr int NP = D / 64;                    // 64-half panels of a row
   static constexpr int TILE = NP * kPanel;             // bytes of a 128 x D tile of halves
-  // Table entries of 8 bytes {x, y | z, z} (fp16), replicated so that the
-  // lanes of a half-warp meet few bank conflicts: every signed code for
-  // b <= 3, the directions alone for b = 4 (8192 codes would fill 64 KB
-  // without a replica), times the norm level from a second table.
-  static constexpr bool SPLIT = B == 4;
-  static constexpr int NE = SPLIT ? K::NDIR : 1 << K::C;
-  static constexpr int REP = NE <= 128 ? 16 : 4;
-  static constexpr int SH = 3 + (REP == 16 ? 4 : 2);   // log2 bytes of an entry with its replicas
-  static constexpr int GS = 3;                         // gamma rows in flight
+  // Table entries of 8 bytes {x, y | z, z} (fp16), 16 copies of each so that
+  // the lanes of a half-warp read 16 distinct banks pairs: b = 2 every signed
+  // code; b = 3 the codes of the positive quadrant, b = 4 its directions alone
+  // (to be multiplied by the norm level from a second table): the codebook and
+  // the inverse map are odd in x and in y, so a code's two signs flip sign bits.
+  static constexpr bool SPLIT = B == 4, QUAD = B > 2;
+  static constexpr int NE = B == 2 ? 128 : 256, REP = 16, SH = 3 + 4;  // SH: log2 bytes of an entry with its copies
+  // gamma rows in flight: a row is written when the product of the tile two before is done, and that one may be
+  // issued while the tile before it is still read
+  static constexpr int GS = 4;
   static constexpr int Q = 0, KT = 2 * TILE, V = 4 * TILE, TAB = 6 * TILE, RHO = TAB + (NE << SH);
-  static constexpr int GAM = RHO + (SPLIT ? 8 * 16 * 4 : 0), BARS = GAM + GS * kKeys * 4;
+  static constexpr int GAM = RHO + (SPLIT ? 8 * 8 * 4 : 0), GMAX = GAM + GS * kKeys * 4, EXPS = GMAX + GS * 16,
+                       BARS = EXPS + 256;
   static constexpr int PLACE = BARS + 144, TMEM = PLACE + 40, DIR = PLACE + 64, RHOF = DIR + 128, SMEM = RHOF + 32;
   static_assert(SMEM <= 232448, "shared memory of an SM");
   static constexpr int THREADS = 512;
@@ -211,6 +226,11 @@ struct AttnCfg {
 
 // barriers
 enum { kQF = 0, kSF = 2, kPR = 4, kKF = 6, kKE = 8, kVF = 10, kVE = 12, kVZ = 14, kEND = 16, kBars = 17 };
+
+__device__ __forceinline__ uint32_t bf16_pair(float x, float y) {
+  const __nv_bfloat162 b2 = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&b2);
+}
 
 // ---- decode warps: key tiles ------------------------------------------------
 template <int D, int B>
@@ -221,34 +241,61 @@ __device__ __forceinline__ bool decode_role(const AttnArgs& a, const Place& plac
   constexpr int W = K::W, T = K::T;
   const int n = threadIdx.x & 127, lane = threadIdx.x & 31;
   const uint32_t tab = base + Cfg::TAB + (lane & (Cfg::REP - 1)) * 8;
-  const uint32_t rho = base + Cfg::RHO + (lane & 15) * 4;
-  uint32_t w[W];
-  float gm = 0.0f;
-  // words and gamma of this thread's slot of a tile (0 behind the sequence)
-  auto fetch = [&](const Walk& it, int tile) {
+  const uint32_t rho = base + Cfg::RHO + (lane & 7) * 4;
+  // Words are fetched a tile ahead, and their page id a tile before that: a
+  // page lookup or a first use would otherwise wait for memory every tile.
+  uint32_t w[W], wn[W];
+  float gm = 0.0f, gn = 0.0f;
+  Walk it(a, place);
+  int tile = 0, id = -1;    // the walk's tile, and the page of this thread's slot in it
+  auto look = [&] {
     const int slot = tile * kKeys + n;
+    id = it.on() && slot < it.s.len ? max(0, page_of(a.t, it.i, slot)) : -1;
+  };
+  auto start = [&] {
+    while (it.on() && it.work() == 0) it.next();
+    if (it.on()) tile = it.t0;
+    look();
+  };
+  // words and gamma of this thread's slot of the walk's tile (0 behind the sequence); the walk steps on
+  int valid = 0, vn = 0;    // slots of the current and the next tile that the sequence holds; 0: no tile
+  auto fetch = [&] {
 #pragma unroll
-    for (int k = 0; k < W; ++k) w[k] = 0u;
-    gm = 0.0f;
-    if (slot < it.s.len) {
-      const int pg = max(0, page_of(a.t, it.i, slot));
-      const int64_t row = static_cast<int64_t>(pg) * a.t.n_heads + it.h;
-      const int off = slot % a.t.page_size;
+    for (int k = 0; k < W; ++k) wn[k] = 0u;
+    gn = 0.0f;
+    vn = 0;
+    if (!it.on()) return;
+    vn = it.s.len - tile * kKeys;
+    if (id >= 0) {
+      const int64_t row = static_cast<int64_t>(id) * a.t.n_heads + it.h;
+      const int off = (tile * kKeys + n) % a.t.page_size;
       const uint32_t* p = a.packed + row * W * a.t.page_size + off;
 #pragma unroll
-      for (int k = 0; k < W; ++k) w[k] = __ldg(p + static_cast<int64_t>(k) * a.t.page_size);
-      gm = __ldg(a.gamma + row * a.t.page_size + off);
+      for (int k = 0; k < W; ++k) wn[k] = __ldg(p + static_cast<int64_t>(k) * a.t.page_size);
+      gn = __ldg(a.gamma + row * a.t.page_size + off);
+    }
+    if (++tile < it.t1) {
+      look();
+    } else {
+      it.next();
+      start();
     }
   };
-  int c = 0;
-  Walk it(a, place);
-  while (it.on() && it.work() == 0) it.next();
-  if (it.on()) fetch(it, it.t0);
-  while (it.on()) {
-    for (int tile = it.t0; tile < it.t1; ++tile, ++c) {
+  start();
+  fetch();
+  for (int c = 0; vn != 0; ++c) {
+    {
+#pragma unroll
+      for (int k = 0; k < W; ++k) w[k] = wn[k];
+      gm = gn;
+      valid = vn;
+      fetch();
       const int st = c & 1;
       if (!bar_wait(bars + 8 * (kKE + st), ((c >> 1) & 1) ^ 1)) return false;
       reinterpret_cast<float*>(sm + Cfg::GAM)[(c % Cfg::GS) * kKeys + n] = gm;
+      // the warp's largest |gamma| (as bits: NaN above all)
+      const uint32_t gb = __reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(gm)));
+      if (lane == 0) reinterpret_cast<uint32_t*>(sm + Cfg::GMAX)[(c % Cfg::GS) * 4 + (n >> 5)] = gb;
       unsigned char* kt = sm + Cfg::KT + st * Cfg::TILE;
       // groups of 8 triplets: 24 halves, three 16-byte chunks of the row
 #pragma unroll
@@ -262,21 +309,25 @@ __device__ __forceinline__ bool decode_role(const AttnArgs& a, const Place& plac
             const int i = g0 + 2 * pr + u;
             e[u] = make_uint2(0u, 0u);
             if (i < T) {
+              // code << SH is the byte offset of its direction's entry (b = 2: of its entry)
+              const uint32_t code = code_at<K::C, Cfg::SH>(w, i);
+              uint32_t at = code;
+              if constexpr (Cfg::QUAD) at = code & ((1u << (2 * B + Cfg::SH)) - (1u << Cfg::SH));
+              if constexpr (B == 3) at |= (code >> 2) & (3u << (2 * B + Cfg::SH));  // the norm level's two bits behind
+              asm("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(e[u].x), "=r"(e[u].y) : "r"(tab + at));
               if constexpr (Cfg::SPLIT) {
-                const uint32_t code = code_at<K::C, 0>(w, i);
-                const uint32_t at = (code & (K::NDIR - 1)) << Cfg::SH;
-                asm("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(e[u].x), "=r"(e[u].y) : "r"(tab + at));
                 uint32_t r;
-                asm("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(rho + (code >> K::DIR) * 64));
+                asm("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(rho + ((code >> (K::DIR + Cfg::SH)) << 5)));
                 const __half2 r2 = *reinterpret_cast<const __half2*>(&r);
                 const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&e[u].x), r2);
                 const __half2 z = __hmul2(*reinterpret_cast<const __half2*>(&e[u].y), r2);
                 e[u].x = *reinterpret_cast<const uint32_t*>(&x);
                 e[u].y = *reinterpret_cast<const uint32_t*>(&z);
-              } else {
-                asm("ld.shared.v2.b32 {%0, %1}, [%2];"
-                    : "=r"(e[u].x), "=r"(e[u].y)
-                    : "r"(tab + code_at<K::C, Cfg::SH>(w, i)));
+              }
+              if constexpr (Cfg::QUAD) {  // s_xi to bit 15, s_eta to bit 31
+                constexpr int sx = 2 * B + Cfg::SH, sy = sx + 1;
+                const uint32_t fx = sx <= 15 ? code << (15 - sx) : code >> (sx - 15);
+                e[u].x ^= (fx & 0x8000u) | ((code << (31 - sy)) & 0x80000000u);
               }
             }
           }
@@ -296,7 +347,6 @@ __device__ __forceinline__ bool decode_role(const AttnArgs& a, const Place& plac
       bar_arrive(bars + 8 * (kKF + st));
       // V rows behind the sequence's end hold whatever the page held: zero
       // them once the copy is in (0 * NaN would reach the output)
-      const int valid = it.s.len - tile * kKeys;
       if (valid < kKeys) {
         if (!bar_wait(bars + 8 * (kVF + st), (c >> 1) & 1)) return false;
         unsigned char* vt = sm + Cfg::V + st * Cfg::TILE;
@@ -308,12 +358,7 @@ __device__ __forceinline__ bool decode_role(const AttnArgs& a, const Place& plac
         fence_async_shared();
         bar_arrive(bars + 8 * (kVZ + st));
       }
-      // next tile's words
-      if (tile + 1 < it.t1) fetch(it, tile + 1);
     }
-    do it.next();
-    while (it.on() && it.work() == 0);
-    if (it.on()) fetch(it, it.t0);
   }
   return true;
 }
@@ -351,124 +396,395 @@ __device__ __forceinline__ bool v_role(const AttnArgs& a, const Place& place, co
 }
 
 // ---- products ---------------------------------------------------------------
-template <int D, int B>
-__device__ __forceinline__ bool mma_role(const AttnArgs& a, const Place& place, uint32_t base, uint32_t bars,
-                                         uint32_t tmem) {
+// S pair TO = query tile QT times the key tile of stage ST; O pair QT (+)=
+// its weights times V of stage ST. Everything but the accumulate flag is a
+// constant over the CTA's base: the issuing thread does little else.
+template <int D, int B, int QT, int TO, int ST>
+__device__ __forceinline__ void issue_qk(uint32_t base) {
   using Cfg = AttnCfg<D, B>;
-  constexpr uint32_t kQK = instr_desc(128, kKeys, false, false), kPV = instr_desc(128, D, true, true);
-  const bool one = (threadIdx.x & 31) == 0;
-  auto qk = [&](int qt, int st) {
+  constexpr uint32_t kDesc = instr_desc(128, kKeys, false, false);
+  const uint32_t q = desc_low(base + Cfg::Q + QT * Cfg::TILE, 16), k = desc_low(base + Cfg::KT + ST * Cfg::TILE, 16);
 #pragma unroll
-    for (int k = 0; k < D / 16; ++k) {
-      const uint32_t off = (k >> 2) * kPanel + (k & 3) * 32;
-      mma_ss(tmem + qt * kKeys, smem_desc(base + Cfg::Q + qt * Cfg::TILE + off, 16),
-             smem_desc(base + Cfg::KT + st * Cfg::TILE + off, 16), kQK, k > 0);
+  for (int s = 0; s < D / 16; ++s) {
+    const uint32_t off = ((s >> 2) * kPanel + (s & 3) * 32) >> 4;
+    if (s == 0)
+      mma_ss<false>(TO * kKeys, q + off, k + off, kDesc);
+    else
+      mma_ss<true>(TO * kKeys, q + off, k + off, kDesc);
+  }
+}
+template <int D, int B, int QT, int ST>
+__device__ __forceinline__ void issue_pv(uint32_t base, bool acc) {
+  using Cfg = AttnCfg<D, B>;
+  constexpr uint32_t kDesc = instr_desc(128, D, true, true);
+  const uint32_t v = desc_low(base + Cfg::V + ST * Cfg::TILE, kPanel);
+#pragma unroll
+  for (int s = 0; s < kKeys / 16; ++s)
+    mma_ts(2 * kKeys + QT * D, QT * kKeys + s * 8, v + (s * 16 * 128 >> 4), kDesc, s > 0 ? 1u : static_cast<uint32_t>(acc));
+}
+
+template <int D, int B>
+__device__ __forceinline__ bool mma_role(const AttnArgs& a, const Place& place, uint32_t base, uint32_t bars) {
+  // phases of the barriers that pass once per item (QF), per softmax (PR) and per tail of V and stage (VZ)
+  int c = 0, nq = 0, np0 = 0, np1 = 0;
+  uint32_t nz = 0;
+  auto v_ready = [&](const Walk& it, int tile) {
+    const int st = c & 1;
+    if (!bar_wait(bars + 8 * (kVF + st), (c >> 1) & 1)) return false;
+    if ((tile + 1) * kKeys > it.s.len) {
+      if (!bar_wait(bars + 8 * (kVZ + st), (nz >> st) & 1)) return false;
+      nz ^= 1u << st;
     }
+    return true;
+  };
+  auto p_ready = [&](int qt) {
+    int& n = qt ? np1 : np0;
+    return bar_wait(bars + 8 * (kPR + qt), n++ & 1);
+  };
+  // S of tile j of the current item (0: query tile 0, 1: query tile 1, of two; 2: the one query tile, into pair `to`)
+  auto qk = [&](int which, int to, int st) {
+    if (elect_one()) {
+      if (which == 1) {
+        if (st) issue_qk<D, B, 1, 1, 1>(base); else issue_qk<D, B, 1, 1, 0>(base);
+      } else if (to) {
+        if (st) issue_qk<D, B, 0, 1, 1>(base); else issue_qk<D, B, 0, 1, 0>(base);
+      } else {
+        if (st) issue_qk<D, B, 0, 0, 1>(base); else issue_qk<D, B, 0, 0, 0>(base);
+      }
+      tc_commit(bars + 8 * (kSF + to));
+    }
+    __syncwarp();
   };
   auto pv = [&](int qt, int st, bool acc) {
-#pragma unroll
-    for (int k = 0; k < kKeys / 16; ++k)
-      mma_ts(tmem + 2 * kKeys + qt * D, tmem + qt * kKeys + k * 8,
-             smem_desc(base + Cfg::V + st * Cfg::TILE + k * 16 * 128, kPanel), kPV, acc || k > 0);
+    if (elect_one()) {
+      if (qt) {
+        if (st) issue_pv<D, B, 1, 1>(base, acc); else issue_pv<D, B, 1, 0>(base, acc);
+      } else {
+        if (st) issue_pv<D, B, 0, 1>(base, acc); else issue_pv<D, B, 0, 0>(base, acc);
+      }
+    }
+    __syncwarp();
   };
-  // phases: query tile 0 takes part in every item, tile 1 in those of more than 128 rows; V tails are per stage
-  int c = 0, nq = 0, np[2] = {0, 0};
-  uint32_t nz = 0;
+  auto commit = [&](int bar) {
+    if (elect_one()) tc_commit(bars + 8 * bar);
+    __syncwarp();
+  };
   for (Walk it(a, place); it.on(); it.next()) {
     const int nt = it.work();
     if (nt == 0) continue;
-    const int tiles2 = it.rows() > 128 ? 2 : 1;
-    for (int qt = 0; qt < tiles2; ++qt)
-      if (!bar_wait(bars + 8 * (kQF + qt), (qt == 0 ? nq : np[1]) & 1)) return false;
+    for (int qt = 0; qt < 2; ++qt)
+      if (!bar_wait(bars + 8 * (kQF + qt), nq & 1)) return false;
     ++nq;
-    if (tiles2 == 2) ++np[1];
     if (!bar_wait(bars + 8 * (kKF + (c & 1)), (c >> 1) & 1)) return false;
     tc_after();
-    if (one) {
-      for (int qt = 0; qt < tiles2; ++qt) {
-        qk(qt, c & 1);
-        tc_commit(bars + 8 * (kSF + qt));
-      }
-      tc_commit(bars + 8 * (kKE + (c & 1)));
-    }
-    __syncwarp();
+    const bool two = it.reps() == 0;
+    qk(0, 0, c & 1);
+    if (two) qk(1, 1, c & 1);
+    commit(kKE + (c & 1));
     for (int j = 0; j < nt; ++j, ++c) {
       const int st = c & 1, sn = st ^ 1;
       const bool more = j + 1 < nt;
       if (more && !bar_wait(bars + 8 * (kKF + sn), ((c + 1) >> 1) & 1)) return false;
-      if (!bar_wait(bars + 8 * (kVF + st), (c >> 1) & 1)) return false;
-      if ((it.t0 + j + 1) * kKeys > it.s.len) {
-        if (!bar_wait(bars + 8 * (kVZ + st), (nz >> st) & 1)) return false;
-        nz ^= 1u << st;
-      }
-      for (int qt = 0; qt < tiles2; ++qt) {
-        if (!bar_wait(bars + 8 * (kPR + qt), (qt == 0 ? c : np[0]) & 1)) return false;
-        tc_after();
-        if (one) {
+      if (two) {
+        if (!v_ready(it, it.t0 + j)) return false;
+        for (int qt = 0; qt < 2; ++qt) {
+          if (!p_ready(qt)) return false;
+          tc_after();
           pv(qt, st, j > 0);
-          if (more) qk(qt, sn);
-          tc_commit(bars + 8 * (kSF + qt));  // S of the next tile, or O after the last
+          if (more)
+            qk(qt, qt, sn);
+          else
+            commit(kSF + qt);  // O is complete
         }
-        __syncwarp();
+        if (more) commit(kKE + sn);
+      } else {
+        // S of the next tile goes to the other pair, whose weights were used a tile ago
+        if (more) {
+          tc_after();
+          qk(0, (j + 1) & 1, sn);
+          commit(kKE + sn);
+        }
+        if (!v_ready(it, it.t0 + j)) return false;
+        if (!p_ready(j & 1)) return false;
+        tc_after();
+        pv(j & 1, st, j > 1);
+        if (!more) {  // both O are complete
+          commit(kSF);
+          commit(kSF + 1);
+        }
       }
-      if (tiles2 == 2) ++np[0];
-      if (one) {
-        tc_commit(bars + 8 * (kVE + st));
-        if (more) tc_commit(bars + 8 * (kKE + sn));
-      }
-      __syncwarp();
+      commit(kVE + st);
     }
   }
   return true;
 }
 
 // ---- softmax warps ----------------------------------------------------------
-// Rotates the queries of this query tile into its shared tile (fp16, scaled
-// by 2^-e per row), a warp per row at a time; lane r of the warp keeps row
-// r's logit factor 2^e * |scale| * log2 e.
-template <int D, int B>
-__device__ __forceinline__ float rotate_queries(const AttnArgs& a, const Walk& it, unsigned char* qtile, int row0,
-                                                int rows, int lane) {
-  constexpr int E = D / 32;
+// Rotates rows first, first + step, ... below `rows` of the item into the
+// query tile (fp16, with the softmax scale and log2 e, and where fp16's range
+// asks for it a power of two per row, whose exponent goes to `exps`); row r lands at tile row r + shift, and `reps` times, `apart` rows
+// apart. A warp takes four rows at a time, so that their loads and shuffles
+// overlap.
+template <int D>
+__device__ __forceinline__ void rotate_queries(const AttnArgs& a, const Walk& it, unsigned char* qtile, int8_t* exps,
+                                               int first, int step, int rows, int shift, int reps, int apart, int lane) {
+  constexpr int E = D / 32, N = 4;
   const float* sg = a.signs + (it.h % a.table_heads) * D + lane * E;
   float sign[E];
-  const float pre = a.scale == 0.0f ? 0.0f : copysignf(1.0f / sqrtf(static_cast<float>(D)), a.scale);
+  const float pre = a.scale * 1.4426950408889634f / sqrtf(static_cast<float>(D));  // logits come in base 2
 #pragma unroll
   for (int e = 0; e < E; ++e) sign[e] = sg[e] * pre;
-  float factor = 1.0f;
-#pragma unroll 4
-  for (int r = 0; r < rows; ++r) {
-    const int rr = it.m * kRows + row0 + r;  // row of the item's (token, group head) list
-    const int tok = rr / a.g, hq = it.h * a.g + rr % a.g;
-    const int64_t off = (it.s.row0 + tok) * a.q_row + hq * a.q_head + lane * E;
-    float v[E];
+#pragma unroll 1
+  for (int r0 = first; r0 < rows; r0 += N * step) {
+    float v[N][E];
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-      v[e] = sign[e] * (a.q_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(a.q)[off + e])
-                                 : static_cast<const float*>(a.q)[off + e]);
-    fwht_warp<E>(v, lane);
-    float mx = 0.0f;
+    for (int k = 0; k < N; ++k) {
+      const int rr = it.m * kRows + min(r0 + k * step, rows - 1);  // row of the sequence's (token, group head) list
+      const int64_t off = (it.s.row0 + rr / a.g) * a.q_row + (it.h * a.g + rr % a.g) * a.q_head + lane * E;
+      if (a.q_bf16) {
+        const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(a.q) + off;
+        if (a.q_vec) {
+          uint32_t x[E / 2];
+          if constexpr (E == 4) {
+            const uint2 y = *reinterpret_cast<const uint2*>(p);
+            x[0] = y.x; x[1] = y.y;
+          } else {
+            x[0] = *reinterpret_cast<const uint32_t*>(p);
+          }
 #pragma unroll
-    for (int e = 0; e < E; ++e) mx = fmaxf(mx, fabsf(v[e]));
-    mx = warp_max(mx);
-    // 2^ex > mx (within 2^-125 .. 2^126, so that 2^-ex is a normal number)
-    const int ex = min(max(static_cast<int>(__float_as_uint(mx) >> 23) - 126, -125), 126);
-    const float down = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
-    uint32_t h[E / 2];
+          for (int e = 0; e < E; ++e) v[k][e] = e & 1 ? bf16_hi(x[e / 2]) : bf16_lo(x[e / 2]);
+        } else {
 #pragma unroll
-    for (int e = 0; e < E; e += 2) h[e / 2] = half2_bits(v[e] * down, v[e + 1] * down);
-    const int row = row0 % 128 + r;
-    unsigned char* p = qtile + sw128(row, lane * E / 8, kPanel) + (lane * E % 8) * 2;
-    if constexpr (E == 4)
-      *reinterpret_cast<uint2*>(p) = make_uint2(h[0], h[1]);
-    else
-      *reinterpret_cast<uint32_t*>(p) = h[0];
-    if (lane == r) {
-      const float sc = a.scale == 0.0f ? 1.0f : fabsf(a.scale);
-      factor = ldexpf(sc * 1.4426950408889634f, ex);
+          for (int e = 0; e < E; ++e) v[k][e] = __bfloat162float(p[e]);
+        }
+      } else {
+        const float* p = static_cast<const float*>(a.q) + off;
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[k][e] = p[e];
+      }
+    }
+    float mx[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[k][e] *= sign[e];
+      fwht_warp<E>(v[k], lane);
+      mx[k] = 0.0f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) mx[k] = fmaxf(mx[k], fabsf(v[k][e]));
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int r = r0 + k * step;
+      const float m = warp_max(mx[k]);
+      // rows whose largest entry lies in [2^-5, 2^14) stay as they are; others are scaled by 2^-ex, 2^ex > m (kept
+      // within 2^-125 .. 2^126, so that it is a normal number)
+      const int ex = (m >= 0x1p-5f && m < 0x1p14f) || m == 0.0f
+                         ? 0 : min(max(static_cast<int>(__float_as_uint(m) >> 23) - 126, -125), 126);
+      const float down = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+      if (r < rows) {
+        uint32_t h[E / 2];
+#pragma unroll
+        for (int e = 0; e < E; e += 2) h[e / 2] = half2_bits(v[k][e] * down, v[k][e + 1] * down);
+        for (int c = 0; c < reps; ++c) {
+          const int row = r + shift + c * apart;
+          unsigned char* p = qtile + sw128(row, lane * E / 8, kPanel) + (lane * E % 8) * 2;
+          if constexpr (E == 4)
+            *reinterpret_cast<uint2*>(p) = make_uint2(h[0], h[1]);
+          else
+            *reinterpret_cast<uint32_t*>(p) = h[0];
+          if (lane == 0) exps[row] = static_cast<int8_t>(ex);
+        }
+      }
     }
   }
-  return factor;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// A row's running state, and the tensor-memory columns of its S (then P) and
+// O. Weights are 2^(logit - ref) for a reference that needs only be near
+// (bf16 and fp32 keep their precision whatever the exponent): it is set by a
+// row's first slots and raised when a logit might pass it by 100.
+template <int D>
+struct Row {
+  uint32_t S, O;
+  float ref, sum, up;  // up: 2^ex of the row's queries
+
+  // Logits less the reference of 32 slots from their raw products: times the norms g.
+  __device__ __forceinline__ void logits(float2 (&y)[16], const uint32_t (&s)[32], const float* gm, float shift) const {
+    const float2 sh = make_float2(shift, shift);
+#pragma unroll
+    for (int x = 0; x < 32; x += 4) {
+      const float4 g = *reinterpret_cast<const float4*>(gm + x);
+      y[x / 2] = fma_f32x2(make_float2(__uint_as_float(s[x]), __uint_as_float(s[x + 1])), make_float2(g.x, g.y), sh);
+      y[x / 2 + 1] =
+          fma_f32x2(make_float2(__uint_as_float(s[x + 2]), __uint_as_float(s[x + 3])), make_float2(g.z, g.w), sh);
+    }
+  }
+  // the same where the row has a scale of its own or does not see all of them (-inf from slot `left` on)
+  __device__ __forceinline__ void logits_any(float2 (&y)[16], uint32_t (&s)[32], const float* gm, int left, float shift) const {
+#pragma unroll
+    for (int x = 0; x < 32; ++x) s[x] = __float_as_uint(__uint_as_float(s[x]) * up);
+    logits(y, s, gm, shift);
+    if (left < 32) {
+#pragma unroll
+      for (int x = 0; x < 16; ++x) {
+        if (2 * x >= left) y[x].x = -INFINITY;
+        if (2 * x + 1 >= left) y[x].y = -INFINITY;
+      }
+    }
+  }
+
+  // bf16 weights of 32 slots to column c of P; their sum
+  __device__ __forceinline__ void weights(const float2 (&y)[16], uint32_t c, float2& total) const {
+    uint32_t p[16];
+#pragma unroll
+    for (int x = 0; x < 16; ++x) {
+      const float2 e = make_float2(ex2(y[x].x), ex2(y[x].y));
+      total = add_f32x2(total, e);
+      p[x] = bf16_pair(e.x, e.y);
+    }
+    tmem_st16(c, p);
+  }
+
+  // A row's reference follows its largest logit of the tile where that passes
+  // it by 16 or is its first; O (o_set: it holds tiles) and the sum follow.
+  __device__ __forceinline__ void follow(float top, bool o_set) {
+    const bool raise = top > ref + 16.0f || (ref == -INFINITY && top > -INFINITY);
+    if (!__any_sync(0xffffffffu, raise)) return;
+    const float keep = raise ? ex2(ref - top) : 1.0f;
+    if (raise) ref = top;
+    sum *= keep;
+    if (o_set) {
+#pragma unroll 1
+      for (int d = 0; d < D; d += 16) {
+        uint32_t o[16];
+        tmem_ld16(o, O + d);
+        tc_wait_ld();
+#pragma unroll
+        for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * keep);
+        tmem_st16(O + d, o);
+      }
+    }
+  }
+
+  __device__ __forceinline__ float largest(const float2 (&y)[16], float top) const {
+#pragma unroll
+    for (int x = 0; x < 16; ++x) top = max3(top, y[x].x, y[x].y);
+    return top;
+  }
+
+  // The weights of columns [col0, col0 + cols) of a key tile, for any row.
+  __device__ __forceinline__ void weigh_any(const float* gm, int col0, int cols, int left, bool o_set) {
+    float top = -INFINITY;
+    uint32_t s[32];
+    float2 y[16];
+#pragma unroll 1
+    for (int c = col0; c < col0 + cols; c += 32) {
+      tmem_ld32(s, S + c);
+      tc_wait_ld();
+      logits_any(y, s, gm + c, left - c, 0.0f);
+      top = largest(y, top);
+    }
+    follow(top, o_set);
+    const float shift = ref == -INFINITY ? 0.0f : -ref;
+    float2 total = make_float2(0.0f, 0.0f);
+#pragma unroll 1
+    for (int c = col0; c < col0 + cols; c += 32) {
+      if (cols > 32) {
+        tmem_ld32(s, S + c);
+        tc_wait_ld();
+        logits_any(y, s, gm + c, left - c, 0.0f);
+      }
+#pragma unroll
+      for (int x = 0; x < 16; ++x) y[x] = add_f32x2(y[x], make_float2(shift, shift));
+      weights(y, S + c / 2, total);
+    }
+    sum += total.x + total.y;
+  }
+
+  // The weights of a whole key tile that every row of the warp sees, scales
+  // all 1. First the largest |product|: times the tile's largest norm it
+  // bounds the logits, and hardly ever asks for a look at the logits
+  // themselves. P's columns overlay S's from the front, so the second half of
+  // S is read first and again at the end.
+  __device__ __forceinline__ void weigh_full(const float* gm, float gmax, bool o_set) {
+    uint32_t s[32], t[32];
+    tmem_ld32(s, S + 64);
+    tmem_ld32(t, S + 96);
+    tc_wait_ld();
+    float top[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int x = 0; x < 32; x += 2) {
+      top[0] = max3(top[0], fabsf(__uint_as_float(s[x])), fabsf(__uint_as_float(s[x + 1])));
+      top[1] = max3(top[1], fabsf(__uint_as_float(t[x])), fabsf(__uint_as_float(t[x + 1])));
+    }
+    tmem_ld32(s, S);
+    tmem_ld32(t, S + 32);
+    tc_wait_ld();
+#pragma unroll
+    for (int x = 0; x < 32; x += 2) {
+      top[0] = max3(top[0], fabsf(__uint_as_float(s[x])), fabsf(__uint_as_float(s[x + 1])));
+      top[1] = max3(top[1], fabsf(__uint_as_float(t[x])), fabsf(__uint_as_float(t[x + 1])));
+    }
+    // (a NaN among them, or an infinite norm, fails the comparison)
+    if (!__all_sync(0xffffffffu, fmaxf(top[0], top[1]) * gmax <= ref + 100.0f)) {
+      float high = -INFINITY;
+      float2 y[16];
+#pragma unroll 1
+      for (int c = 0; c < kKeys; c += 32) {
+        tmem_ld32(s, S + c);
+        tc_wait_ld();
+        logits(y, s, gm + c, 0.0f);
+        high = largest(y, high);
+      }
+      follow(high, o_set);
+      tmem_ld32(s, S);
+      tmem_ld32(t, S + 32);
+      tc_wait_ld();
+    }
+    const float shift = ref == -INFINITY ? 0.0f : -ref;
+    float2 u = make_float2(0.0f, 0.0f), v = make_float2(0.0f, 0.0f), y[16], z[16];
+    logits(y, s, gm, shift);
+    logits(z, t, gm + 32, shift);
+    tmem_ld32(s, S + 64);
+    tmem_ld32(t, S + 96);
+    weights(y, S, u);
+    weights(z, S + 16, v);
+    tc_wait_ld();
+    logits(y, s, gm + 64, shift);
+    logits(z, t, gm + 96, shift);
+    weights(y, S + 32, u);
+    weights(z, S + 48, v);
+    u = add_f32x2(u, v);
+    sum += u.x + u.y;
+  }
+};
+
+// 32 values of an output row: bf16 or fp32.
+__device__ __forceinline__ void store32(const AttnArgs& a, int64_t at, const float (&v)[32]) {
+  if (a.out_bf16) {
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + at);
+#pragma unroll
+    for (int x = 0; x < 32; x += 8) {
+      uint32_t w[4];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const __nv_bfloat162 b2 = __floats2bfloat162_rn(v[x + 2 * y], v[x + 2 * y + 1]);
+        w[y] = *reinterpret_cast<const uint32_t*>(&b2);
+      }
+      dst[x / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  } else {
+    float4* dst = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at);
+#pragma unroll
+    for (int x = 0; x < 32; x += 4) dst[x / 4] = make_float4(v[x], v[x + 1], v[x + 2], v[x + 3]);
+  }
 }
 
 template <int D, int B>
@@ -477,120 +793,61 @@ __device__ __forceinline__ bool softmax_role(const AttnArgs& a, const Place& pla
   using Cfg = AttnCfg<D, B>;
   const int warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
   const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
-  const uint32_t S = tmem + lanes + qt * kKeys, O = tmem + lanes + 2 * kKeys + qt * D;
+  int8_t* exps = reinterpret_cast<int8_t*>(sm + Cfg::EXPS);
+  const float* gam = reinterpret_cast<const float*>(sm + Cfg::GAM);
+  Row<D> row;
+  row.S = tmem + lanes + qt * kKeys;
+  row.O = tmem + lanes + 2 * kKeys + qt * D;
   int c = 0, ns = 0;
   for (Walk it(a, place); it.on(); it.next()) {
-    const int nt = it.work(), rows = it.rows();
-    const bool mine = qt == 0 || rows > 128;  // this query tile takes part in the item
-    if (!mine) {
-      c += nt;
-      continue;
-    }
-    const int r0 = qt * 128 + warp * 32;                     // first row of the warp
-    const int wr = min(32, max(0, rows - r0));               // its rows
-    const int rr = it.m * kRows + r0 + lane;
+    const int nt = it.work(), rows = it.rows(), reps = it.reps();
+    const bool two = reps == 0;
+    // this thread's row of the item, and the warp's share of a key tile: columns [col0, col0 + cols)
+    const int apart = two ? 128 : 128 / reps;       // rows of a copy
+    const int r0 = two ? qt * 128 + warp * 32 : warp * 32 % apart, x = r0 + lane;
+    const int cols = two ? kKeys : kKeys / reps, col0 = two ? 0 : warp * 32 / apart * cols;
+    const int wr = min(32, max(0, rows - r0));      // rows of the warp
     const bool there = lane < wr;
+    const int rr = it.m * kRows + x;
     int limit = 0;
     if (there) limit = a.causal ? max(0, it.s.len - it.s.fresh + rr / a.g + 1) : it.s.len;
-    float ref = -INFINITY, sum = 0.0f;
+    row.ref = -INFINITY;
+    row.sum = 0.0f;
     if (nt > 0) {
-      const float factor = rotate_queries<D, B>(a, it, sm + Cfg::Q + qt * Cfg::TILE, r0, wr, lane);
+      if (two) {
+        rotate_queries<D>(a, it, sm + Cfg::Q + qt * Cfg::TILE, exps + qt * 128, r0, 1, r0 + wr, -qt * 128, 1, 0, lane);
+        __syncwarp();
+      } else {
+        rotate_queries<D>(a, it, sm + Cfg::Q, exps, qt * 4 + warp, 8, rows, 0, reps, apart, lane);
+        named_sync<1, 256>();
+      }
       fence_async_shared();
       bar_arrive(bars + 8 * (kQF + qt));
-      for (int j = 0; j < nt; ++j, ++c) {
+      const int ex = there ? exps[(two ? qt * 128 : 0) + warp * 32 + lane] : 0;
+      row.up = ldexpf(1.0f, ex);
+      const bool plain = __all_sync(0xffffffffu, ex == 0);
+      for (int j = two ? 0 : qt; j < nt; j += two ? 1 : 2) {
         if (!bar_wait(bars + 8 * (kSF + qt), ns & 1)) return false;
         ++ns;
         tc_after();
         if (wr > 0) {  // a warp without rows leaves its part of P as it is: those rows go nowhere
-          const float* gm = reinterpret_cast<const float*>(sm + Cfg::GAM) + (c % Cfg::GS) * kKeys;
+          const float* gm = gam + ((c + j) % Cfg::GS) * kKeys;
           const int left = limit - (it.t0 + j) * kKeys;  // slots of the tile that the row sees
           const bool masked = __any_sync(0xffffffffu, there && left < kKeys);
-          // two halves of 64 slots, so that a row's logits stay in registers from the maximum to the weights
+          const bool o_set = two ? j > 0 : j > 1;
+          if (cols == kKeys && plain && !masked) {
+            const float4 g4 = *reinterpret_cast<const float4*>(sm + Cfg::GMAX + ((c + j) % Cfg::GS) * 16);
+            row.weigh_full(gm, max3(g4.x, g4.y, fmaxf(g4.z, g4.w)), o_set);
+          } else {
+            row.weigh_any(gm, col0, cols, left, o_set);
+          }
+          if (cols < kKeys) {
+            uint32_t zero[16];
+#pragma unroll
+            for (int y = 0; y < 16; ++y) zero[y] = 0u;
 #pragma unroll 1
-          for (int half = 0; half < 2; ++half) {
-            uint32_t s[2][32];
-            tmem_ld32(s[0], S + half * 64);
-            tmem_ld32(s[1], S + half * 64 + 32);
-            tc_wait_ld();
-            float top[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-#pragma unroll
-              for (int x = 0; x < 32; x += 4) {
-                const float4 g4 = *reinterpret_cast<const float4*>(gm + half * 64 + k * 32 + x);
-                const float2 lo = mul_f32x2(make_float2(__uint_as_float(s[k][x]), __uint_as_float(s[k][x + 1])),
-                                            make_float2(g4.x, g4.y));
-                const float2 hi = mul_f32x2(make_float2(__uint_as_float(s[k][x + 2]), __uint_as_float(s[k][x + 3])),
-                                            make_float2(g4.z, g4.w));
-                s[k][x] = __float_as_uint(lo.x);
-                s[k][x + 1] = __float_as_uint(lo.y);
-                s[k][x + 2] = __float_as_uint(hi.x);
-                s[k][x + 3] = __float_as_uint(hi.y);
-              }
-            }
-            if (masked) {
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-#pragma unroll
-                for (int x = 0; x < 32; ++x)
-                  if (half * 64 + k * 32 + x >= left) s[k][x] = 0xff800000u;  // -inf
-              }
-            }
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-#pragma unroll
-              for (int x = 0; x < 32; x += 2)
-                top[k] = fmaxf(top[k], fmaxf(__uint_as_float(s[k][x]), __uint_as_float(s[k][x + 1])));
-            }
-            const float high = fmaxf(top[0], top[1]) * factor;  // factor > 0
-            const bool raise = high > ref + kRaise || (ref == -INFINITY && high > -INFINITY);
-            if (__any_sync(0xffffffffu, raise)) {
-              const float keep = raise ? ex2(ref - high) : 1.0f;
-              if (raise) ref = high;
-              sum *= keep;
-              if (j > 0) {
-#pragma unroll 1
-                for (int k = 0; k < D; k += 16) {
-                  uint32_t o[16];
-                  tmem_ld16(o, O + k);
-                  tc_wait_ld();
-#pragma unroll
-                  for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * keep);
-                  tmem_st16(O + k, o);
-                }
-              }
-              if (half == 1) {  // the first half's weights follow
-#pragma unroll 1
-                for (int k = 0; k < 32; k += 16) {
-                  uint32_t o[16];
-                  tmem_ld16(o, S + k);
-                  tc_wait_ld();
-#pragma unroll
-                  for (int x = 0; x < 16; ++x) {
-                    const __nv_bfloat162 b2 = __floats2bfloat162_rn(bf16_lo(o[x]) * keep, bf16_hi(o[x]) * keep);
-                    o[x] = *reinterpret_cast<const uint32_t*>(&b2);
-                  }
-                  tmem_st16(S + k, o);
-                }
-              }
-            }
-            const float shift = ref == -INFINITY ? 0.0f : -ref;
-            float2 part = make_float2(0.0f, 0.0f);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              uint32_t p[16];
-#pragma unroll
-              for (int x = 0; x < 32; x += 2) {
-                const float2 y = fma_f32x2(make_float2(__uint_as_float(s[k][x]), __uint_as_float(s[k][x + 1])),
-                                           make_float2(factor, factor), make_float2(shift, shift));
-                const float2 e = make_float2(ex2(y.x), ex2(y.y));
-                part = add_f32x2(part, e);
-                const __nv_bfloat162 b2 = __floats2bfloat162_rn(e.x, e.y);
-                p[x / 2] = *reinterpret_cast<const uint32_t*>(&b2);
-              }
-              tmem_st16(S + half * 32 + k * 16, p);
-            }
-            sum += part.x + part.y;
+            for (int k = 0; k < kKeys; k += 32)
+              if (k < col0 || k >= col0 + cols) tmem_st16(row.S + k / 2, zero);
           }
           tc_wait_st();
         }
@@ -601,53 +858,110 @@ __device__ __forceinline__ bool softmax_role(const AttnArgs& a, const Place& pla
       ++ns;
       tc_after();
     }
+    c += nt;
     // ---- results of the item (or of this piece of it)
     const bool whole = it.t0 == 0 && it.t1 == it.tiles;
-    const int64_t slot = 2 * blockIdx.x + (it.t0 > 0 ? 0 : 1);
-    const int64_t prow = slot * a.slot_rows + r0 + lane;
-    const int tok = rr / a.g, hq = it.h * a.g + rr % a.g;
-    const int64_t orow = static_cast<int64_t>(it.s.row0 + tok) * a.Hq + hq;
-    if (wr > 0) {
-      const float inv = whole ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f;
-      if (there) {
-        if (!whole)
-          a.part_ml[prow] = make_float2(ref, sum);
-        else if (a.lse)
-          a.lse[orow] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
-      }
-#pragma unroll 1
-      for (int k = 0; k < D; k += 32) {
-        uint32_t o[32];
-        if (nt > 0) {
-          tmem_ld32(o, O + k);
-          tc_wait_ld();
-        }
-#pragma unroll
-        for (int x = 0; x < 32; ++x) {
-          const float v = nt > 0 ? __uint_as_float(o[x]) * inv : 0.0f;
-          o[x] = __float_as_uint(sum == 0.0f ? 0.0f : v);  // a row that saw nothing: its P rows were all 0 or never written
-        }
+    const int64_t prow = (2 * static_cast<int64_t>(blockIdx.x) + (it.t0 > 0 ? 0 : 1)) * a.slot_rows;
+    const int64_t row_at = static_cast<int64_t>(it.s.row0) * a.Hq + static_cast<int64_t>(it.h) * a.g;
+    auto out_row = [&](int y) {  // row y of the item in out and lse
+      const int q = it.m * kRows + y;
+      return row_at + static_cast<int64_t>(q / a.g) * a.Hq + q % a.g;
+    };
+    if (two || nt == 0) {
+      if (wr > 0 && (two || qt == 0) && (two || warp * 32 < apart)) {
+        const float sum = row.sum, inv = whole ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f;
+        const int64_t orow = out_row(x);
         if (there) {
-          if (whole && a.out_bf16) {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + orow * D + k);
+          if (!whole)
+            a.part_ml[prow + x] = make_float2(row.ref, sum);
+          else if (a.lse)
+            a.lse[orow] = sum == 0.0f ? -INFINITY : (row.ref + log2f(sum)) * 0.6931471805599453f;
+        }
+#pragma unroll 1
+        for (int k = 0; k < D; k += 32) {
+          uint32_t o[32];
+          float v[32];
+          if (nt > 0) {
+            tmem_ld32(o, row.O + k);
+            tc_wait_ld();
+          }
+          // a row that saw nothing gives 0
 #pragma unroll
-            for (int x = 0; x < 32; x += 8) {
-              uint32_t w[4];
+          for (int y = 0; y < 32; ++y) v[y] = nt == 0 || sum == 0.0f ? 0.0f : __uint_as_float(o[y]) * inv;
+          if (there) {
+            if (whole) {
+              store32(a, orow * D + k, v);
+            } else {
+              float4* dst = reinterpret_cast<float4*>(a.part_o + (prow + x) * D + k);
 #pragma unroll
-              for (int y = 0; y < 4; ++y) {
-                const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(o[x + 2 * y]), __uint_as_float(o[x + 2 * y + 1]));
-                w[y] = *reinterpret_cast<const uint32_t*>(&b2);
-              }
-              dst[x / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+              for (int y = 0; y < 32; y += 4) dst[y / 4] = make_float4(v[y], v[y + 1], v[y + 2], v[y + 3]);
             }
-          } else {
-            float* dst = whole ? static_cast<float*>(a.out) + orow * D + k : a.part_o + prow * D + k;
-#pragma unroll
-            for (int x = 0; x < 32; x += 4)
-              *reinterpret_cast<uint4*>(dst + x) = make_uint4(o[x], o[x + 1], o[x + 2], o[x + 3]);
           }
         }
       }
+    } else {
+      // the copies of each row: references and sums through shared memory (the second query tile is free), O scaled
+      // to the common reference through this CTA's rows in the workspace, summed in a fixed order
+      float2* ml = reinterpret_cast<float2*>(sm + Cfg::Q + Cfg::TILE);  // [2][128] of the copies, then [128] of the rows
+      const int me = qt * 128 + warp * 32 + lane;
+      ml[me] = there ? make_float2(row.ref, row.sum) : make_float2(-INFINITY, 0.0f);
+      named_sync<1, 256>();
+      float top = -INFINITY, all = 0.0f;
+      for (int k = 0; k < 2 * reps; ++k) top = fmaxf(top, ml[(k & 1) * 128 + (k >> 1) * apart + x].x);
+      const float base = top == -INFINITY ? 0.0f : top;
+      for (int k = 0; k < 2 * reps; ++k) {
+        const float2 y = ml[(k & 1) * 128 + (k >> 1) * apart + x];
+        all = fmaf(ex2(y.x - base), y.y, all);
+      }
+      if (qt == 0 && warp * 32 < apart) ml[256 + x] = make_float2(top, all);
+      float* mine = a.copies + (static_cast<int64_t>(blockIdx.x) * 256 + me) * D;
+      if (wr > 0) {
+        const float keep = row.sum == 0.0f ? 0.0f : ex2(row.ref - base);
+#pragma unroll 1
+        for (int k = 0; k < D; k += 32) {
+          uint32_t o[32];
+          tmem_ld32(o, row.O + k);
+          tc_wait_ld();
+          if (there) {
+#pragma unroll
+            for (int y = 0; y < 32; y += 4) {
+              float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              if (row.sum != 0.0f)  // a copy without a slot may hold anything
+                v = make_float4(__uint_as_float(o[y]) * keep, __uint_as_float(o[y + 1]) * keep,
+                                __uint_as_float(o[y + 2]) * keep, __uint_as_float(o[y + 3]) * keep);
+              *reinterpret_cast<float4*>(mine + k + y) = v;
+            }
+          }
+        }
+      }
+      named_sync<1, 256>();
+      const int tid = threadIdx.x & 255;
+      for (int e = tid; e < rows * (D / 4); e += 256) {
+        const int y = e / (D / 4), d = e % (D / 4) * 4;
+        const float2 t = ml[256 + y];
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        const float* src = a.copies + (static_cast<int64_t>(blockIdx.x) * 256 + y) * D + d;
+        for (int k = 0; k < 2 * reps; ++k) {
+          const float4 v = *reinterpret_cast<const float4*>(src + static_cast<int64_t>((k & 1) * 128 + (k >> 1) * apart) * D);
+          o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
+        }
+        if (whole) {
+          const int64_t orow = out_row(y);
+          const float inv = t.y == 0.0f ? 0.0f : 1.0f / t.y;
+          if (a.out_bf16) {
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + orow * D + d) =
+                make_uint2(bf16_pair(o.x * inv, o.y * inv), bf16_pair(o.z * inv, o.w * inv));
+          } else {
+            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + orow * D + d) =
+                make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+          }
+          if (a.lse && d == 0) a.lse[orow] = t.y == 0.0f ? -INFINITY : (t.x + log2f(t.y)) * 0.6931471805599453f;
+        } else {
+          *reinterpret_cast<float4*>(a.part_o + (prow + y) * D + d) = o;
+          if (d == 0) a.part_ml[prow + y] = t;
+        }
+      }
+      named_sync<1, 256>();
     }
     tc_before();
   }
@@ -692,22 +1006,23 @@ __global__ void __launch_bounds__(512, 1) paged_attn_kernel(const __grid_constan
   __syncthreads();
   const Place place = s_place;
   if (place.count > 0) {
-    // decoded codes (b = 4: directions) in fp16, Cfg::REP copies of each
+    // decoded codes (b = 4: directions) in fp16, and their copies
     for (int e = tid; e < Cfg::NE; e += Cfg::THREADS) {
-      const float3 d = field_direction<B>(e & (K::NDIR - 1), s_dir);
-      const float r = Cfg::SPLIT ? 1.0f : s_rho[e >> K::DIR];
+      const int field = Cfg::QUAD ? e & ((1 << 2 * B) - 1) : e & (K::NDIR - 1);
+      const float3 d = field_direction<B>(field, s_dir);
+      const float r = Cfg::SPLIT ? 1.0f : s_rho[Cfg::QUAD ? e >> (2 * B) : e >> K::DIR];
       const uint2 v = make_uint2(half2_bits(d.x * r, d.y * r), half2_bits(d.z * r, d.z * r));
 #pragma unroll
       for (int k = 0; k < Cfg::REP; ++k)
         *reinterpret_cast<uint2*>(sm + Cfg::TAB + (e << Cfg::SH) + k * 8) = v;
     }
-    if (Cfg::SPLIT && tid < 128)
-      *reinterpret_cast<uint32_t*>(sm + Cfg::RHO + tid * 4) = half2_bits(s_rho[tid >> 4], s_rho[tid >> 4]);
+    if (Cfg::SPLIT && tid < 64)
+      *reinterpret_cast<uint32_t*>(sm + Cfg::RHO + tid * 4) = half2_bits(s_rho[tid >> 3], s_rho[tid >> 3]);
   }
   tc_before();
   __syncthreads();
   tc_after();
-  const uint32_t tmem = s_tmem;
+  constexpr uint32_t tmem = 0;  // the allocation is the whole tensor memory, so it starts at column 0
   bool ok = true;
   if (place.count > 0) {
     if (warp < 8) {
@@ -719,7 +1034,7 @@ __global__ void __launch_bounds__(512, 1) paged_attn_kernel(const __grid_constan
     } else {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
       if (warp == 12) {
-        ok = mma_role<D, B>(a, place, base, bars, tmem);
+        ok = mma_role<D, B>(a, place, base, bars);
         // products in flight end before tensor memory is given back
         if (!ok) {
           if (lane == 0) tc_commit(bars + 8 * kEND);
@@ -737,7 +1052,7 @@ __global__ void __launch_bounds__(512, 1) paged_attn_kernel(const __grid_constan
   if (!ok && lane == 0) report(a.t.status, OCTO_PAGED_TIMEOUT);
   tc_before();
   __syncthreads();
-  if (warp == 12) tmem_free(tmem, 512);
+  if (warp == 12) tmem_free(s_tmem, 512);
 }
 
 // ---- joining the pieces of shared items --------------------------------------
@@ -883,8 +1198,8 @@ extern "C" size_t octo_paged_attn_workspace(const octo_layout* L, int64_t n_rows
   using namespace octo::paged;
   if (check_layout(L) != OCTO_OK || L->d > 128 || n_rows < 0 || n_seqs < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0)
     return 0;
-  const size_t rows = static_cast<size_t>(2) * sm_count() * slot_rows(n_rows, Hq / Hkv);
-  return 256 + rows * (static_cast<size_t>(L->d) * sizeof(float) + sizeof(float2));
+  const size_t ctas = sm_count(), rows = 2 * ctas * slot_rows(n_rows, Hq / Hkv);
+  return 256 + rows * (L->d * sizeof(float) + sizeof(float2)) + ctas * 256 * L->d * sizeof(float);
 }
 
 extern "C" int octo_paged_attn(const octo_layout* L, const octo_tables* tab, const octo_pages* pages,
@@ -940,6 +1255,9 @@ extern "C" int octo_paged_attn(const octo_layout* L, const octo_tables* tab, con
   a.part_ml = reinterpret_cast<float2*>(workspace);
   const size_t ml = (static_cast<size_t>(2) * ctas * a.slot_rows * sizeof(float2) + 255) / 256 * 256;
   a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + ml);
+  a.copies = a.part_o + static_cast<size_t>(2) * ctas * a.slot_rows * L->d;
+  const int qe = q_dtype == OCTO_BF16 ? 2 : 4, lane = L->d / 32 * qe;  // bytes of a lane's query values
+  a.q_vec = reinterpret_cast<uintptr_t>(q) % lane == 0 && q_row_stride * qe % lane == 0 && q_head_stride * qe % lane == 0;
   // V comes in boxes that lie inside one page: the largest power of two (8-row swizzle groups) that divides it
   a.box = 16;
   while (a.box < kKeys && pages->page_size % (2 * a.box) == 0) a.box *= 2;

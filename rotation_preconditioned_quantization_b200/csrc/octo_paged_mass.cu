@@ -374,11 +374,29 @@ __device__ __forceinline__ bool mass_copies(const MassArgs& a, const UnitPlace& 
   return true;
 }
 
-template <int D, int B>
-__device__ __forceinline__ bool mass_products(const MassArgs& a, const UnitPlace& place, uint32_t base, uint32_t bars,
-                                              uint32_t tmem) {
+// S^T of one half (HALF) from the query tile of stage ST, N columns; small
+// products first. Descriptors are constants over the CTA's base.
+template <int D, int B, int HALF, int ST>
+__device__ __forceinline__ void issue_scores(uint32_t base, uint32_t idesc) {
   using Cfg = MassCfg<D, B>;
-  const bool one = (threadIdx.x & 31) == 0;
+  constexpr uint32_t d = (HALF * 2 + ST) * kQRows;
+#pragma unroll
+  for (int part = 0; part < 3; ++part) {
+    const uint32_t k = desc_low(base + Cfg::KB + HALF * 2 * Cfg::KT + (part == 0 ? Cfg::KT : 0), 16);
+    const uint32_t q = desc_low(base + Cfg::QB + ST * 2 * Cfg::QT + (part == 1 ? Cfg::QT : 0), 16);
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) {
+      const uint32_t ko = ((s >> 2) * kKPanel + (s & 3) * 32) >> 4, qo = ((s >> 2) * kQPanel + (s & 3) * 32) >> 4;
+      if (part + s == 0)
+        mma_ss<false>(d, k + ko, q + qo, idesc);
+      else
+        mma_ss<true>(d, k + ko, q + qo, idesc);
+    }
+  }
+}
+
+template <int D, int B>
+__device__ __forceinline__ bool mass_products(const MassArgs& a, const UnitPlace& place, uint32_t base, uint32_t bars) {
   int c = 0, k = 0;
   for (Units it(a, place); it.on(); it.next()) {
     if (it.first >= it.tiles) continue;
@@ -390,17 +408,11 @@ __device__ __forceinline__ bool mass_products(const MassArgs& a, const UnitPlace
         if (m == it.first && !bar_wait(bars + 8 * (mKF + half), k & 1)) return false;
         if (!bar_wait(bars + 8 * (mDE + half * 2 + st), ((c >> 1) & 1) ^ 1)) return false;
         tc_after();
-        if (one) {
-          const uint32_t d = tmem + (half * 2 + st) * kQRows;
-          const uint32_t kh = base + Cfg::KB + half * 2 * Cfg::KT, qh = base + Cfg::QB + st * 2 * Cfg::QT;
-          // small products first
-#pragma unroll
-          for (int part = 0; part < 3; ++part) {
-            const uint32_t ka = part == 0 ? kh + Cfg::KT : kh, qa = part == 1 ? qh + Cfg::QT : qh;
-#pragma unroll
-            for (int s = 0; s < D / 16; ++s)
-              mma_ss(d, smem_desc(ka + (s >> 2) * kKPanel + (s & 3) * 32, 16),
-                     smem_desc(qa + (s >> 2) * kQPanel + (s & 3) * 32, 16), idesc, part + s > 0);
+        if (elect_one()) {
+          if (half) {
+            if (st) issue_scores<D, B, 1, 1>(base, idesc); else issue_scores<D, B, 1, 0>(base, idesc);
+          } else {
+            if (st) issue_scores<D, B, 0, 1>(base, idesc); else issue_scores<D, B, 0, 0>(base, idesc);
           }
           tc_commit(bars + 8 * (mDF + half * 2 + st));
           if (m + 1 == it.tiles) tc_commit(bars + 8 * (mKE + half));
@@ -497,7 +509,7 @@ __global__ void __launch_bounds__(576, 1) paged_mass_kernel(const __grid_constan
     }
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 16) tmem_alloc(s32(&s_tmem), 256);
+  if (warp == 16) tmem_alloc(s32(&s_tmem), 512);
   __syncthreads();
   const UnitPlace place = s_place;
   if (place.count > 0) {
@@ -520,7 +532,7 @@ __global__ void __launch_bounds__(576, 1) paged_mass_kernel(const __grid_constan
   tc_before();
   __syncthreads();
   tc_after();
-  const uint32_t tmem = s_tmem;
+  constexpr uint32_t tmem = 0;  // the allocation is the whole tensor memory, so it starts at column 0
   bool ok = true;
   if (place.count > 0) {
     if (warp < 8) {
@@ -528,7 +540,7 @@ __global__ void __launch_bounds__(576, 1) paged_mass_kernel(const __grid_constan
     } else if (warp < 16) {
       ok = mass_decode<D, B>(a, place, sm, base, bars, (warp - 8) >> 2);
     } else if (warp == 16) {
-      ok = mass_products<D, B>(a, place, base, bars, tmem);
+      ok = mass_products<D, B>(a, place, base, bars);
       if (!ok) {  // products in flight end before tensor memory is given back (a fresh barrier in the table's place)
         if (lane == 0) {
           bar_init(base + Cfg::PLACE, 1);
@@ -549,7 +561,7 @@ __global__ void __launch_bounds__(576, 1) paged_mass_kernel(const __grid_constan
   if (!ok && lane == 0) report(a.t.status, OCTO_PAGED_TIMEOUT);
   tc_before();
   __syncthreads();
-  if (warp == 16) tmem_free(tmem, 256);
+  if (warp == 16) tmem_free(s_tmem, 512);
 }
 
 // ---- host -------------------------------------------------------------------------
