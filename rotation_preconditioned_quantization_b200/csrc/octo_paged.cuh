@@ -51,28 +51,41 @@ struct Table {
   const int32_t* pages;
   int64_t stride;
   int32_t n_seqs, max_pages, page_size, n_heads;
+  int32_t page_shift;  // log2 page_size where that is a power of two, else -1
   int64_t n_pages;
   int32_t* status;
 };
 
 inline Table make_table(const octo_pages* p, const octo_page_table* t) {
-  return Table{t->pages, t->stride, t->n_seqs, t->max_pages, p->page_size, p->n_heads, p->n_pages, p->status};
+  int shift = 0;
+  while ((p->page_size >> shift) > 1) ++shift;
+  if ((1 << shift) != p->page_size) shift = -1;
+  return Table{t->pages, t->stride, t->n_seqs, t->max_pages, p->page_size, p->n_heads, shift, p->n_pages, p->status};
 }
 
 __device__ __forceinline__ void report(int32_t* status, int bits) {
   if (status) atomicOr(status, bits);
 }
 
-// Page of slot s of sequence i, or -1 (reported) when the id is outside the
-// pool. s must be below max_pages * page_size.
-__device__ __forceinline__ int page_of(const Table& t, int i, int s) {
-  const int id = __ldg(t.pages + static_cast<int64_t>(i) * t.stride + s / t.page_size);
-  if (id < 0 || id >= t.n_pages) {
-    report(t.status, OCTO_PAGED_BAD_PAGE);
-    return -1;
-  }
-  return id;
+// Table index and offset of a slot (an integer division only for page sizes
+// that are no power of two).
+__device__ __forceinline__ int page_index(const Table& t, int s) {
+  return t.page_shift >= 0 ? s >> t.page_shift : s / t.page_size;
 }
+__device__ __forceinline__ int page_offset(const Table& t, int s) {
+  return t.page_shift >= 0 ? s & (t.page_size - 1) : s % t.page_size;
+}
+// A page id read from the table, or -1 (reported) when it is outside the pool.
+__device__ __forceinline__ int page_checked(const Table& t, int id) {
+  if (id >= 0 && id < t.n_pages) return id;
+  report(t.status, OCTO_PAGED_BAD_PAGE);
+  return -1;
+}
+__device__ __forceinline__ const int32_t* page_entry(const Table& t, int i, int s) {
+  return t.pages + static_cast<int64_t>(i) * t.stride + page_index(t, s);
+}
+// Page of slot s of sequence i, or -1 (reported). s must be below max_pages * page_size.
+__device__ __forceinline__ int page_of(const Table& t, int i, int s) { return page_checked(t, __ldg(page_entry(t, i, s))); }
 
 // Rows of the chunk and cache length of one sequence, clamped to what the
 // tables hold.
@@ -89,6 +102,14 @@ __device__ __forceinline__ Seq seq_of(const Table& t, const int32_t* seq_lens, c
   s.len = min(max(n, 0), cap);
   if (tell && (s.row0 != a || s.fresh != z - a || s.len != n)) report(t.status, OCTO_PAGED_BAD_LENGTH);
   return s;
+}
+
+// A load that starts here: the compiler neither moves it to its use nor the
+// use to it.
+__device__ __forceinline__ uint32_t load_now(const void* p) {
+  uint32_t v;
+  asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
 }
 
 // ---- mbarriers --------------------------------------------------------------
@@ -162,12 +183,11 @@ __device__ __forceinline__ uint32_t desc_low(uint32_t addr, uint32_t lead) { ret
 // One product of kind f16, D (fp32, tensor memory) (+)= A * B, by one thread.
 // The issue rate of that thread bounds short products, so the descriptors are
 // sums of a uniform word and a constant. A in shared memory, or in tensor memory.
-template <bool ACC>
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
   asm volatile(
       "{\n .reg .pred p;\n .reg .b64 x, y;\n setp.ne.u32 p, %5, 0;\n mov.b64 x, {%1, %4};\n mov.b64 y, {%2, %4};\n"
       " tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "r"(b), "r"(idesc), "n"(kDescHigh), "n"(ACC ? 1 : 0)
+      "r"(a), "r"(b), "r"(idesc), "n"(kDescHigh), "r"(acc)
       : "memory");
 }
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
@@ -262,8 +282,8 @@ __device__ __forceinline__ uint32_t half2_bits(float x, float y) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Bits [at - SH, at + C) of a key's words as code << SH (the byte offset of a
-// table entry of 1 << SH bytes); at = i * C, all compile-time.
+// Code i (0..7) of a key's stream as code << SH (the byte offset of a table
+// entry of 1 << SH bytes).
 template <int C, int SH, int W>
 __device__ __forceinline__ uint32_t code_at(const uint32_t (&w)[W], int i) {
   constexpr uint32_t mask = ((1u << C) - 1u) << SH;
@@ -272,6 +292,18 @@ __device__ __forceinline__ uint32_t code_at(const uint32_t (&w)[W], int i) {
   const int q = p >> 5, s = p & 31;
   if (s + C + SH <= 32 || q + 1 >= W) return (w[q] >> s) & mask;
   return __funnelshift_r(w[q], w[q + 1], s) & mask;
+}
+// The stream 8 codes on. Decode loops take 8 triplets at a time and shift,
+// rather than unroll over the key: unrolled, the roles' code did not fit the
+// instruction caches together, and a third of the warps' time went to fetches.
+template <int C, int W>
+__device__ __forceinline__ void next_codes(uint32_t (&w)[W]) {
+  constexpr int q = 8 * C / 32, s = 8 * C % 32;
+#pragma unroll
+  for (int k = 0; k < W; ++k) {
+    const uint32_t lo = k + q < W ? w[k + q] : 0u, hi = k + q + 1 < W ? w[k + q + 1] : 0u;
+    w[k] = s == 0 ? lo : __funnelshift_r(lo, hi, s);
+  }
 }
 
 }  // namespace paged

@@ -47,6 +47,7 @@ namespace paged {
 
 constexpr int kRows = 256;   // query rows of an item
 constexpr int kKeys = 128;   // slots of a key tile
+constexpr int kJoin = 256;   // CTAs that may share an item: the launch has no more
 constexpr int kPanel = 128 * 128;  // bytes of a 128-row panel of 64 halves
 
 struct AttnArgs {
@@ -238,7 +239,7 @@ __device__ __forceinline__ bool decode_role(const AttnArgs& a, const Place& plac
                                             uint32_t bars) {
   using Cfg = AttnCfg<D, B>;
   using K = Code<D, B>;
-  constexpr int W = K::W, T = K::T;
+  constexpr int W = K::W;
   const int n = threadIdx.x & 127, lane = threadIdx.x & 31;
   const uint32_t tab = base + Cfg::TAB + (lane & (Cfg::REP - 1)) * 8;
   const uint32_t rho = base + Cfg::RHO + (lane & 7) * 4;
@@ -247,10 +248,12 @@ __device__ __forceinline__ bool decode_role(const AttnArgs& a, const Place& plac
   uint32_t w[W], wn[W];
   float gm = 0.0f, gn = 0.0f;
   Walk it(a, place);
-  int tile = 0, id = -1;    // the walk's tile, and the page of this thread's slot in it
+  int tile = 0, id = 0;     // the walk's tile, and the page of this thread's slot in it (as read: checked at its use)
+  bool held = false;        // the sequence holds that slot
   auto look = [&] {
     const int slot = tile * kKeys + n;
-    id = it.on() && slot < it.s.len ? max(0, page_of(a.t, it.i, slot)) : -1;
+    held = it.on() && slot < it.s.len;
+    if (held) id = static_cast<int>(load_now(page_entry(a.t, it.i, slot)));
   };
   auto start = [&] {
     while (it.on() && it.work() == 0) it.next();
@@ -266,13 +269,13 @@ __device__ __forceinline__ bool decode_role(const AttnArgs& a, const Place& plac
     vn = 0;
     if (!it.on()) return;
     vn = it.s.len - tile * kKeys;
-    if (id >= 0) {
-      const int64_t row = static_cast<int64_t>(id) * a.t.n_heads + it.h;
-      const int off = (tile * kKeys + n) % a.t.page_size;
+    if (held) {
+      const int64_t row = static_cast<int64_t>(max(0, page_checked(a.t, id))) * a.t.n_heads + it.h;
+      const int off = page_offset(a.t, tile * kKeys + n);
       const uint32_t* p = a.packed + row * W * a.t.page_size + off;
 #pragma unroll
-      for (int k = 0; k < W; ++k) wn[k] = __ldg(p + static_cast<int64_t>(k) * a.t.page_size);
-      gn = __ldg(a.gamma + row * a.t.page_size + off);
+      for (int k = 0; k < W; ++k) wn[k] = load_now(p + static_cast<int64_t>(k) * a.t.page_size);
+      gn = __uint_as_float(load_now(a.gamma + row * a.t.page_size + off));
     }
     if (++tile < it.t1) {
       look();
@@ -298,17 +301,17 @@ __device__ __forceinline__ bool decode_role(const AttnArgs& a, const Place& plac
       if (lane == 0) reinterpret_cast<uint32_t*>(sm + Cfg::GMAX)[(c % Cfg::GS) * 4 + (n >> 5)] = gb;
       unsigned char* kt = sm + Cfg::KT + st * Cfg::TILE;
       // groups of 8 triplets: 24 halves, three 16-byte chunks of the row
-#pragma unroll
-      for (int g0 = 0; g0 < T; g0 += 8) {
+      constexpr int GROUPS = (D + 23) / 24;
+#pragma unroll 1
+      for (int grp = 0; grp < GROUPS; ++grp) {
         uint32_t o[12];
 #pragma unroll
         for (int pr = 0; pr < 4; ++pr) {
           uint2 e[2];
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            const int i = g0 + 2 * pr + u;
-            e[u] = make_uint2(0u, 0u);
-            if (i < T) {
+            const int i = 2 * pr + u;
+            {  // (codes behind the key's last are zeros of the stream, and their halves go nowhere)
               // code << SH is the byte offset of its direction's entry (b = 2: of its entry)
               const uint32_t code = code_at<K::C, Cfg::SH>(w, i);
               uint32_t at = code;
@@ -337,11 +340,12 @@ __device__ __forceinline__ bool decode_role(const AttnArgs& a, const Place& plac
         }
 #pragma unroll
         for (int q = 0; q < 3; ++q) {
-          const int chunk = g0 / 8 * 3 + q;
+          const int chunk = grp * 3 + q;
           if (chunk < D / 8)
             *reinterpret_cast<uint4*>(kt + sw128(n, chunk, kPanel)) =
                 make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
         }
+        next_codes<K::C>(w);
       }
       fence_async_shared();
       bar_arrive(bars + 8 * (kKF + st));
@@ -386,7 +390,7 @@ __device__ __forceinline__ bool v_role(const AttnArgs& a, const Place& place, co
         const int pg = max(0, page_of(a.t, it.i, slot));
 #pragma unroll
         for (int p = 0; p < Cfg::NP; ++p)
-          tma_3d(base + Cfg::V + st * Cfg::TILE + p * kPanel + b * a.box * 128, map, p * 64, slot % a.t.page_size,
+          tma_3d(base + Cfg::V + st * Cfg::TILE + p * kPanel + b * a.box * 128, map, p * 64, page_offset(a.t, slot),
                  pg * a.t.n_heads + it.h, bars + 8 * (kVF + st));
       }
       __syncwarp();
@@ -396,35 +400,33 @@ __device__ __forceinline__ bool v_role(const AttnArgs& a, const Place& place, co
 }
 
 // ---- products ---------------------------------------------------------------
-// S pair TO = query tile QT times the key tile of stage ST; O pair QT (+)=
-// its weights times V of stage ST. Everything but the accumulate flag is a
-// constant over the CTA's base: the issuing thread does little else.
-template <int D, int B, int QT, int TO, int ST>
-__device__ __forceinline__ void issue_qk(uint32_t base) {
-  using Cfg = AttnCfg<D, B>;
+// S = query tile times key tile; O (+)= weights times V. One copy of each in
+// the code (it shares the instruction caches with the other roles).
+template <int D>
+__device__ __noinline__ void issue_qk(uint32_t s_col, uint32_t q, uint32_t k) {
   constexpr uint32_t kDesc = instr_desc(128, kKeys, false, false);
-  const uint32_t q = desc_low(base + Cfg::Q + QT * Cfg::TILE, 16), k = desc_low(base + Cfg::KT + ST * Cfg::TILE, 16);
+  if (elect_one()) {
 #pragma unroll
-  for (int s = 0; s < D / 16; ++s) {
-    const uint32_t off = ((s >> 2) * kPanel + (s & 3) * 32) >> 4;
-    if (s == 0)
-      mma_ss<false>(TO * kKeys, q + off, k + off, kDesc);
-    else
-      mma_ss<true>(TO * kKeys, q + off, k + off, kDesc);
+    for (int s = 0; s < D / 16; ++s) {
+      const uint32_t off = ((s >> 2) * kPanel + (s & 3) * 32) >> 4;
+      mma_ss(s_col, q + off, k + off, kDesc, s > 0);
+    }
   }
+  __syncwarp();
 }
-template <int D, int B, int QT, int ST>
-__device__ __forceinline__ void issue_pv(uint32_t base, bool acc) {
-  using Cfg = AttnCfg<D, B>;
+template <int D>
+__device__ __noinline__ void issue_pv(uint32_t o_col, uint32_t p_col, uint32_t v, uint32_t acc) {
   constexpr uint32_t kDesc = instr_desc(128, D, true, true);
-  const uint32_t v = desc_low(base + Cfg::V + ST * Cfg::TILE, kPanel);
+  if (elect_one()) {
 #pragma unroll
-  for (int s = 0; s < kKeys / 16; ++s)
-    mma_ts(2 * kKeys + QT * D, QT * kKeys + s * 8, v + (s * 16 * 128 >> 4), kDesc, s > 0 ? 1u : static_cast<uint32_t>(acc));
+    for (int s = 0; s < kKeys / 16; ++s) mma_ts(o_col, p_col + s * 8, v + (s * 16 * 128 >> 4), kDesc, s > 0 ? 1u : acc);
+  }
+  __syncwarp();
 }
 
 template <int D, int B>
 __device__ __forceinline__ bool mma_role(const AttnArgs& a, const Place& place, uint32_t base, uint32_t bars) {
+  using Cfg = AttnCfg<D, B>;
   // phases of the barriers that pass once per item (QF), per softmax (PR) and per tail of V and stage (VZ)
   int c = 0, nq = 0, np0 = 0, np1 = 0;
   uint32_t nz = 0;
@@ -441,33 +443,16 @@ __device__ __forceinline__ bool mma_role(const AttnArgs& a, const Place& place, 
     int& n = qt ? np1 : np0;
     return bar_wait(bars + 8 * (kPR + qt), n++ & 1);
   };
-  // S of tile j of the current item (0: query tile 0, 1: query tile 1, of two; 2: the one query tile, into pair `to`)
-  auto qk = [&](int which, int to, int st) {
-    if (elect_one()) {
-      if (which == 1) {
-        if (st) issue_qk<D, B, 1, 1, 1>(base); else issue_qk<D, B, 1, 1, 0>(base);
-      } else if (to) {
-        if (st) issue_qk<D, B, 0, 1, 1>(base); else issue_qk<D, B, 0, 1, 0>(base);
-      } else {
-        if (st) issue_qk<D, B, 0, 0, 1>(base); else issue_qk<D, B, 0, 0, 0>(base);
-      }
-      tc_commit(bars + 8 * (kSF + to));
-    }
-    __syncwarp();
-  };
-  auto pv = [&](int qt, int st, bool acc) {
-    if (elect_one()) {
-      if (qt) {
-        if (st) issue_pv<D, B, 1, 1>(base, acc); else issue_pv<D, B, 1, 0>(base, acc);
-      } else {
-        if (st) issue_pv<D, B, 0, 1>(base, acc); else issue_pv<D, B, 0, 0>(base, acc);
-      }
-    }
-    __syncwarp();
-  };
   auto commit = [&](int bar) {
     if (elect_one()) tc_commit(bars + 8 * bar);
     __syncwarp();
+  };
+  auto qk = [&](int qt, int to, int st) {  // query tile qt into S pair `to`
+    issue_qk<D>(to * kKeys, desc_low(base + Cfg::Q + qt * Cfg::TILE, 16), desc_low(base + Cfg::KT + st * Cfg::TILE, 16));
+    commit(kSF + to);
+  };
+  auto pv = [&](int qt, int st, bool acc) {
+    issue_pv<D>(2 * kKeys + qt * D, qt * kKeys, desc_low(base + Cfg::V + st * Cfg::TILE, kPanel), acc);
   };
   for (Walk it(a, place); it.on(); it.next()) {
     const int nt = it.work();
@@ -711,26 +696,20 @@ struct Row {
   // The weights of a whole key tile that every row of the warp sees, scales
   // all 1. First the largest |product|: times the tile's largest norm it
   // bounds the logits, and hardly ever asks for a look at the logits
-  // themselves. P's columns overlay S's from the front, so the second half of
-  // S is read first and again at the end.
+  // themselves.
   __device__ __forceinline__ void weigh_full(const float* gm, float gmax, bool o_set) {
     uint32_t s[32], t[32];
-    tmem_ld32(s, S + 64);
-    tmem_ld32(t, S + 96);
-    tc_wait_ld();
     float top[2] = {0.0f, 0.0f};
+#pragma unroll 1
+    for (int c = 0; c < kKeys; c += 64) {
+      tmem_ld32(s, S + c);
+      tmem_ld32(t, S + c + 32);
+      tc_wait_ld();
 #pragma unroll
-    for (int x = 0; x < 32; x += 2) {
-      top[0] = max3(top[0], fabsf(__uint_as_float(s[x])), fabsf(__uint_as_float(s[x + 1])));
-      top[1] = max3(top[1], fabsf(__uint_as_float(t[x])), fabsf(__uint_as_float(t[x + 1])));
-    }
-    tmem_ld32(s, S);
-    tmem_ld32(t, S + 32);
-    tc_wait_ld();
-#pragma unroll
-    for (int x = 0; x < 32; x += 2) {
-      top[0] = max3(top[0], fabsf(__uint_as_float(s[x])), fabsf(__uint_as_float(s[x + 1])));
-      top[1] = max3(top[1], fabsf(__uint_as_float(t[x])), fabsf(__uint_as_float(t[x + 1])));
+      for (int x = 0; x < 32; x += 2) {
+        top[0] = max3(top[0], fabsf(__uint_as_float(s[x])), fabsf(__uint_as_float(s[x + 1])));
+        top[1] = max3(top[1], fabsf(__uint_as_float(t[x])), fabsf(__uint_as_float(t[x + 1])));
+      }
     }
     // (a NaN among them, or an infinite norm, fails the comparison)
     if (!__all_sync(0xffffffffu, fmaxf(top[0], top[1]) * gmax <= ref + 100.0f)) {
@@ -744,23 +723,20 @@ struct Row {
         high = largest(y, high);
       }
       follow(high, o_set);
-      tmem_ld32(s, S);
-      tmem_ld32(t, S + 32);
-      tc_wait_ld();
     }
     const float shift = ref == -INFINITY ? 0.0f : -ref;
-    float2 u = make_float2(0.0f, 0.0f), v = make_float2(0.0f, 0.0f), y[16], z[16];
-    logits(y, s, gm, shift);
-    logits(z, t, gm + 32, shift);
-    tmem_ld32(s, S + 64);
-    tmem_ld32(t, S + 96);
-    weights(y, S, u);
-    weights(z, S + 16, v);
-    tc_wait_ld();
-    logits(y, s, gm + 64, shift);
-    logits(z, t, gm + 96, shift);
-    weights(y, S + 32, u);
-    weights(z, S + 48, v);
+    float2 u = make_float2(0.0f, 0.0f), v = make_float2(0.0f, 0.0f);
+#pragma unroll 1
+    for (int c = 0; c < kKeys; c += 64) {  // P's columns overlay S's from the front: behind those read here
+      float2 y[16];
+      tmem_ld32(s, S + c);
+      tmem_ld32(t, S + c + 32);
+      tc_wait_ld();
+      logits(y, s, gm + c, shift);
+      weights(y, S + c / 2, u);
+      logits(y, t, gm + c + 32, shift);
+      weights(y, S + c / 2 + 16, v);
+    }
     u = add_f32x2(u, v);
     sum += u.x + u.y;
   }
@@ -1026,13 +1002,10 @@ __global__ void __launch_bounds__(512, 1) paged_attn_kernel(const __grid_constan
   bool ok = true;
   if (place.count > 0) {
     if (warp < 8) {
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
       ok = softmax_role<D, B>(a, place, sm, bars, tmem, warp >> 2);
     } else if (warp < 12) {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 112;");
       ok = decode_role<D, B>(a, place, sm, base, bars);
     } else {
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
       if (warp == 12) {
         ok = mma_role<D, B>(a, place, base, bars);
         // products in flight end before tensor memory is given back
@@ -1100,43 +1073,64 @@ __global__ void __launch_bounds__(256) paged_attn_join(const __grid_constant__ A
   const int64_t at = s_at, end = at + item_tiles(s, a.g, a.causal, m);
   // the CTA that holds list position p is the last whose piece starts at or before it
   auto owner = [&](int64_t p) { return static_cast<int>(((p + 1) * ctas + total - 1) / total - 1); };
-  const int c0 = owner(at), c1 = owner(end - 1);
-  if (c0 == c1) return;  // written whole
-  auto part_row = [&](int c, int r) {
-    return (2 * static_cast<int64_t>(c) + (at < c * total / ctas ? 0 : 1)) * a.slot_rows + r;
-  };
-  constexpr int TPR = D / 4, RPB = 256 / TPR;  // threads per row, rows at a time
-  for (int r = r0 + tid / TPR; r < min(rows, r0 + 32); r += RPB) {
-    const int x = (tid % TPR) * 4;
+  const int c0 = owner(at), n = owner(end - 1) - c0 + 1;
+  if (n == 1) return;  // written whole
+  // the pieces' first partial rows, and their weights for the rows of this block
+  __shared__ int64_t s_row[kJoin];
+  __shared__ float s_w[kJoin][32];
+  __shared__ float s_ref[32], s_sum[32];
+  for (int k = tid; k < n; k += 256)
+    s_row[k] = (2 * static_cast<int64_t>(c0 + k) + (at < (c0 + k) * total / ctas ? 0 : 1)) * a.slot_rows + r0;
+  __syncthreads();
+  const int nr = min(32, rows - r0);
+  {  // eight threads per row
+    const int r = tid >> 3, part = tid & 7;
     float ref = -INFINITY;
-    for (int c = c0; c <= c1; ++c) ref = fmaxf(ref, a.part_ml[part_row(c, r)].x);
+    if (r < nr)
+      for (int k = part; k < n; k += 8) ref = fmaxf(ref, a.part_ml[s_row[k] + r].x);
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, o));
     const float base = ref == -INFINITY ? 0.0f : ref;
     float sum = 0.0f;
+    if (r < nr)
+      for (int k = part; k < n; k += 8) {
+        const float2 ml = a.part_ml[s_row[k] + r];
+        const float w = ex2(ml.x - base);
+        s_w[k][r] = w;
+        sum = fmaf(w, ml.y, sum);
+      }
+#pragma unroll
+    for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (part == 0 && r < nr) {
+      s_ref[r] = ref;
+      s_sum[r] = sum;
+    }
+  }
+  __syncthreads();
+  constexpr int TPR = D / 4, RPB = 256 / TPR;  // threads per row, rows at a time
+  for (int r = tid / TPR; r < nr; r += RPB) {
+    const int x = (tid % TPR) * 4;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-    for (int c = c0; c <= c1; ++c) {
-      const int64_t pr = part_row(c, r);
-      const float2 ml = a.part_ml[pr];
-      const float4 v = *reinterpret_cast<const float4*>(a.part_o + pr * D + x);
-      const float w = ex2(ml.x - base);
-      sum = fmaf(w, ml.y, sum);
+#pragma unroll 8
+    for (int k = 0; k < n; ++k) {
+      const float4 v = *reinterpret_cast<const float4*>(a.part_o + (s_row[k] + r) * D + x);
+      const float w = s_w[k][r];
       o.x = fmaf(w, v.x, o.x);
       o.y = fmaf(w, v.y, o.y);
       o.z = fmaf(w, v.z, o.z);
       o.w = fmaf(w, v.w, o.w);
     }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    const int rr = m * kRows + r, hq = h * a.g + rr % a.g;
+    const float sum = s_sum[r], inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const int rr = m * kRows + r0 + r, hq = h * a.g + rr % a.g;
     const int64_t orow = static_cast<int64_t>(s.row0 + rr / a.g) * a.Hq + hq;
     if (a.out_bf16) {
-      const __nv_bfloat162 lo = __floats2bfloat162_rn(o.x * inv, o.y * inv), hi = __floats2bfloat162_rn(o.z * inv, o.w * inv);
       *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + orow * D + x) =
-          make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+          make_uint2(bf16_pair(o.x * inv, o.y * inv), bf16_pair(o.z * inv, o.w * inv));
     } else {
       *reinterpret_cast<float4*>(static_cast<float*>(a.out) + orow * D + x) =
           make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
     }
-    if (a.lse && x == 0) a.lse[orow] = sum == 0.0f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
+    if (a.lse && x == 0) a.lse[orow] = sum == 0.0f ? -INFINITY : (s_ref[r] + log2f(sum)) * 0.6931471805599453f;
   }
 }
 
@@ -1151,6 +1145,8 @@ static int sm_count() {
   if (cached) known[dev].store(sms, std::memory_order_relaxed);
   return sms;
 }
+
+static int attn_ctas() { return std::min(sm_count(), kJoin); }
 
 static bool encode_v_map(CUtensorMap* m, const octo_pages* p, int D, int box) {
   static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
@@ -1198,7 +1194,7 @@ extern "C" size_t octo_paged_attn_workspace(const octo_layout* L, int64_t n_rows
   using namespace octo::paged;
   if (check_layout(L) != OCTO_OK || L->d > 128 || n_rows < 0 || n_seqs < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0)
     return 0;
-  const size_t ctas = sm_count(), rows = 2 * ctas * slot_rows(n_rows, Hq / Hkv);
+  const size_t ctas = attn_ctas(), rows = 2 * ctas * slot_rows(n_rows, Hq / Hkv);
   return 256 + rows * (L->d * sizeof(float) + sizeof(float2)) + ctas * 256 * L->d * sizeof(float);
 }
 
@@ -1250,7 +1246,7 @@ extern "C" int octo_paged_attn(const octo_layout* L, const octo_tables* tab, con
   a.out = out;
   a.out_bf16 = out_dtype == OCTO_BF16;
   a.lse = lse;
-  const int ctas = sm_count();
+  const int ctas = attn_ctas();
   a.slot_rows = slot_rows(n_rows, g);
   a.part_ml = reinterpret_cast<float2*>(workspace);
   const size_t ml = (static_cast<size_t>(2) * ctas * a.slot_rows * sizeof(float2) + 255) / 256 * 256;

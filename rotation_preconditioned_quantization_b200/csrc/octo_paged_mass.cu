@@ -281,7 +281,7 @@ __device__ __forceinline__ bool mass_decode(const MassArgs& a, const UnitPlace& 
     for (int k = 0; k < W; ++k) w[k] = 0u;
     if (slot < it.s.len) {
       const int pg = max(0, page_of(a.t, it.i, slot));
-      const uint32_t* p = a.packed + (static_cast<int64_t>(pg) * a.t.n_heads + it.h) * W * a.t.page_size + slot % a.t.page_size;
+      const uint32_t* p = a.packed + (static_cast<int64_t>(pg) * a.t.n_heads + it.h) * W * a.t.page_size + page_offset(a.t, slot);
 #pragma unroll
       for (int k = 0; k < W; ++k) w[k] = __ldg(p + static_cast<int64_t>(k) * a.t.page_size);
     }
@@ -387,10 +387,7 @@ __device__ __forceinline__ void issue_scores(uint32_t base, uint32_t idesc) {
 #pragma unroll
     for (int s = 0; s < D / 16; ++s) {
       const uint32_t ko = ((s >> 2) * kKPanel + (s & 3) * 32) >> 4, qo = ((s >> 2) * kQPanel + (s & 3) * 32) >> 4;
-      if (part + s == 0)
-        mma_ss<false>(d, k + ko, q + qo, idesc);
-      else
-        mma_ss<true>(d, k + ko, q + qo, idesc);
+      mma_ss(d, k + ko, q + qo, idesc, part + s > 0);
     }
   }
 }
@@ -440,7 +437,7 @@ __device__ __forceinline__ bool mass_sums(const MassArgs& a, const UnitPlace& pl
     float gamma = 0.0f, mass = 0.0f;
     if (held) {
       const int pg = max(0, page_of(a.t, it.i, slot));
-      gamma = __ldg(a.gamma + (static_cast<int64_t>(pg) * a.t.n_heads + it.h) * a.t.page_size + slot % a.t.page_size);
+      gamma = __ldg(a.gamma + (static_cast<int64_t>(pg) * a.t.n_heads + it.h) * a.t.page_size + page_offset(a.t, slot));
     }
     if (kept && a.mass_in) mass = a.decay * a.mass_in[at];
     if (held && !kept) report(a.t.status, OCTO_PAGED_BAD_LENGTH);

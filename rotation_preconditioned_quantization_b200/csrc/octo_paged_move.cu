@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(256) paged_write_kernel(const __grid_constant_
     const bool held = r >= __ldg(a.cu + lo) && r < __ldg(a.cu + lo + 1);
     if (held && slot >= 0 && slot < static_cast<int64_t>(a.t.max_pages) * a.t.page_size) {
       const int pg = page_of(a.t, lo, static_cast<int>(slot));
-      if (pg >= 0) to = (static_cast<int64_t>(pg) * a.t.n_heads + h) * a.t.page_size + slot % a.t.page_size;
+      if (pg >= 0) to = (static_cast<int64_t>(pg) * a.t.n_heads + h) * a.t.page_size + page_offset(a.t, static_cast<int>(slot));
     } else {
       report(a.t.status, OCTO_PAGED_BAD_LENGTH);
     }
@@ -265,10 +265,10 @@ __global__ void __launch_bounds__(256) paged_gather_kernel(const __grid_constant
     if (slot >= 0) {
       const int pg = page_of(a.src, i, slot), z = page_of(a.dst, i, k0 + t);
       if (pg >= 0) {
-        row = (static_cast<int64_t>(pg) * a.src.n_heads + h) * P + slot % P;
-        from = (static_cast<int64_t>(pg) * a.src.n_heads + h) * a.m.W * P + slot % P;
+        row = (static_cast<int64_t>(pg) * a.src.n_heads + h) * P + page_offset(a.src, slot);
+        from = (static_cast<int64_t>(pg) * a.src.n_heads + h) * a.m.W * P + page_offset(a.src, slot);
       }
-      if (z >= 0) to = (static_cast<int64_t>(z) * a.src.n_heads + h) * P + (k0 + t) % P;
+      if (z >= 0) to = (static_cast<int64_t>(z) * a.src.n_heads + h) * P + page_offset(a.dst, k0 + t);
     }
     s_src[t] = from;
     s_srow[t] = row;
