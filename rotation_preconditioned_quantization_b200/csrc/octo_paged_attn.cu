@@ -207,18 +207,21 @@ struct AttnCfg {
   using K = Code<D, B>;
   static constexpr int NP = D / 64;                    // 64-half panels of a row
   static constexpr int TILE = NP * kPanel;             // bytes of a 128 x D tile of halves
-  // Table entries of 8 bytes {x, y | z, z} (fp16), 16 copies of each so that
-  // the lanes of a half-warp read 16 distinct banks pairs: b = 2 every signed
-  // code; b = 3 the codes of the positive quadrant, b = 4 its directions alone
-  // (to be multiplied by the norm level from a second table): the codebook and
-  // the inverse map are odd in x and in y, so a code's two signs flip sign bits.
-  static constexpr bool SPLIT = B == 4, QUAD = B > 2;
-  static constexpr int NE = B == 2 ? 128 : 256, REP = 16, SH = 3 + 4;  // SH: log2 bytes of an entry with its copies
+  // Table entries of 8 bytes {x, y | z, z} (fp16). b = 2 and 3: every signed
+  // code, copied 16 and 4 times (the lanes of a half-warp then meet none or
+  // two to three in a bank; the positive quadrant alone, copied 16 times, met
+  // none at b = 3 too, but restoring the signs cost more than the banks).
+  // b = 4 (8192 codes): the positive quadrant's directions, copied 16 times,
+  // multiplied by the norm level from a second table; the codebook and the
+  // inverse map are odd in x and in y, so the signs flip sign bits.
+  static constexpr bool QUAD = B == 4;
+  static constexpr int NE = B == 2 ? 128 : B == 3 ? 1024 : 256, REP = B == 3 ? 4 : 16;
+  static constexpr int SH = 3 + (REP == 16 ? 4 : 2);  // log2 bytes of an entry with its copies
   // gamma rows in flight: a row is written when the product of the tile two before is done, and that one may be
   // issued while the tile before it is still read
   static constexpr int GS = 4;
   static constexpr int Q = 0, KT = 2 * TILE, V = 4 * TILE, TAB = 6 * TILE, RHO = TAB + (NE << SH);
-  static constexpr int GAM = RHO + (SPLIT ? 8 * 8 * 4 : 0), GMAX = GAM + GS * kKeys * 4, EXPS = GMAX + GS * 16,
+  static constexpr int GAM = RHO + (QUAD ? 8 * 8 * 4 : 0), GMAX = GAM + GS * kKeys * 4, EXPS = GMAX + GS * 16,
                        BARS = EXPS + 256;
   static constexpr int PLACE = BARS + 144, TMEM = PLACE + 40, DIR = PLACE + 64, RHOF = DIR + 128, SMEM = RHOF + 32;
   static_assert(SMEM <= 232448, "shared memory of an SM");
@@ -241,8 +244,7 @@ __device__ __forceinline__ bool decode_role(const AttnArgs& a, const Place& plac
   using K = Code<D, B>;
   constexpr int W = K::W;
   const int n = threadIdx.x & 127, lane = threadIdx.x & 31;
-  const uint32_t tab = base + Cfg::TAB + (lane & (Cfg::REP - 1)) * 8;
-  const uint32_t rho = base + Cfg::RHO + (lane & 7) * 4;
+  const uint32_t copy = (lane & (Cfg::REP - 1)) * 8, rcopy = (lane & 7) * 4;  // this lane's copies of the tables
   // Words are fetched a tile ahead, and their page id a tile before that: a
   // page lookup or a first use would otherwise wait for memory every tile.
   uint32_t w[W], wn[W];
@@ -312,25 +314,20 @@ __device__ __forceinline__ bool decode_role(const AttnArgs& a, const Place& plac
           for (int u = 0; u < 2; ++u) {
             const int i = 2 * pr + u;
             {  // (codes behind the key's last are zeros of the stream, and their halves go nowhere)
-              // code << SH is the byte offset of its direction's entry (b = 2: of its entry)
+              // code << SH is the byte offset of its entry (QUAD: of its direction's, without the signs)
               const uint32_t code = code_at<K::C, Cfg::SH>(w, i);
               uint32_t at = code;
               if constexpr (Cfg::QUAD) at = code & ((1u << (2 * B + Cfg::SH)) - (1u << Cfg::SH));
-              if constexpr (B == 3) at |= (code >> 2) & (3u << (2 * B + Cfg::SH));  // the norm level's two bits behind
-              asm("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(e[u].x), "=r"(e[u].y) : "r"(tab + at));
-              if constexpr (Cfg::SPLIT) {
-                uint32_t r;
-                asm("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(rho + ((code >> (K::DIR + Cfg::SH)) << 5)));
-                const __half2 r2 = *reinterpret_cast<const __half2*>(&r);
+              e[u] = *reinterpret_cast<const uint2*>(sm + Cfg::TAB + (at | copy));
+              if constexpr (Cfg::QUAD) {
+                const __half2 r2 = *reinterpret_cast<const __half2*>(
+                    sm + Cfg::RHO + (((code >> (K::DIR + Cfg::SH - 5)) & 0xe0u) | rcopy));
                 const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&e[u].x), r2);
                 const __half2 z = __hmul2(*reinterpret_cast<const __half2*>(&e[u].y), r2);
                 e[u].x = *reinterpret_cast<const uint32_t*>(&x);
                 e[u].y = *reinterpret_cast<const uint32_t*>(&z);
-              }
-              if constexpr (Cfg::QUAD) {  // s_xi to bit 15, s_eta to bit 31
-                constexpr int sx = 2 * B + Cfg::SH, sy = sx + 1;
-                const uint32_t fx = sx <= 15 ? code << (15 - sx) : code >> (sx - 15);
-                e[u].x ^= (fx & 0x8000u) | ((code << (31 - sy)) & 0x80000000u);
+                constexpr int sx = 2 * B + Cfg::SH, sy = sx + 1;  // s_xi to bit 15, s_eta to bit 31
+                e[u].x ^= ((code << (15 - sx)) & 0x8000u) | ((code << (31 - sy)) & 0x80000000u);
               }
             }
           }
@@ -590,6 +587,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
+// largest magnitude
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+  float d;
+  asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 
 // A row's running state, and the tensor-memory columns of its S (then P) and
 // O. Weights are 2^(logit - ref) for a reference that needs only be near
@@ -707,8 +710,8 @@ struct Row {
       tc_wait_ld();
 #pragma unroll
       for (int x = 0; x < 32; x += 2) {
-        top[0] = max3(top[0], fabsf(__uint_as_float(s[x])), fabsf(__uint_as_float(s[x + 1])));
-        top[1] = max3(top[1], fabsf(__uint_as_float(t[x])), fabsf(__uint_as_float(t[x + 1])));
+        top[0] = max3_abs(top[0], __uint_as_float(s[x]), __uint_as_float(s[x + 1]));
+        top[1] = max3_abs(top[1], __uint_as_float(t[x]), __uint_as_float(t[x + 1]));
       }
     }
     // (a NaN among them, or an infinite norm, fails the comparison)
@@ -986,13 +989,13 @@ __global__ void __launch_bounds__(512, 1) paged_attn_kernel(const __grid_constan
     for (int e = tid; e < Cfg::NE; e += Cfg::THREADS) {
       const int field = Cfg::QUAD ? e & ((1 << 2 * B) - 1) : e & (K::NDIR - 1);
       const float3 d = field_direction<B>(field, s_dir);
-      const float r = Cfg::SPLIT ? 1.0f : s_rho[Cfg::QUAD ? e >> (2 * B) : e >> K::DIR];
+      const float r = Cfg::QUAD ? 1.0f : s_rho[(e >> K::DIR) & (K::NRHO - 1)];
       const uint2 v = make_uint2(half2_bits(d.x * r, d.y * r), half2_bits(d.z * r, d.z * r));
 #pragma unroll
       for (int k = 0; k < Cfg::REP; ++k)
         *reinterpret_cast<uint2*>(sm + Cfg::TAB + (e << Cfg::SH) + k * 8) = v;
     }
-    if (Cfg::SPLIT && tid < 64)
+    if (Cfg::QUAD && tid < 64)
       *reinterpret_cast<uint32_t*>(sm + Cfg::RHO + tid * 4) = half2_bits(s_rho[tid >> 3], s_rho[tid >> 3]);
   }
   tc_before();
