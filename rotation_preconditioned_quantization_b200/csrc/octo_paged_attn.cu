@@ -62,7 +62,7 @@ struct AttnArgs {
   const int32_t* cu;
   const void* q;
   int64_t q_row, q_head, n_rows;
-  int q_bf16, q_vec, Hq, g, causal, box;  // q_vec: a lane's D / 32 query values are one aligned access; box: V rows per copy
+  int q_bf16, q_vec, Hq, g, causal, box;  // q_vec: query rows allow 16-byte loads; box: V rows per copy
   float scale;
   void* out;
   int out_bf16;
@@ -502,82 +502,80 @@ __device__ __forceinline__ bool mma_role(const AttnArgs& a, const Place& place, 
 }
 
 // ---- softmax warps ----------------------------------------------------------
-// Rotates rows first, first + step, ... below `rows` of the item into the
-// query tile (fp16, with the softmax scale and log2 e, and where fp16's range
-// asks for it a power of two per row, whose exponent goes to `exps`); row r lands at tile row r + shift, and `reps` times, `apart` rows
-// apart. A warp takes four rows at a time, so that their loads and shuffles
-// overlap.
+// Rotates rows first .. last - 1 of the item into the query tile (fp16, with
+// the softmax scale and log2 e, and where fp16's range asks for it a power of
+// two per row, whose exponent goes to `exps`); row r lands at tile row r +
+// shift, and `reps` times, `apart` rows apart. D / 32 lanes hold a row, so a
+// warp takes 1024 / D rows at a time, `step` rows apart from the next.
 template <int D>
 __device__ __forceinline__ void rotate_queries(const AttnArgs& a, const Walk& it, unsigned char* qtile, int8_t* exps,
-                                               int first, int step, int rows, int shift, int reps, int apart, int lane) {
-  constexpr int E = D / 32, N = 4;
-  const float* sg = a.signs + (it.h % a.table_heads) * D + lane * E;
-  float sign[E];
+                                               int first, int step, int last, int shift, int reps, int apart, int lane) {
+  constexpr int LK = D / 32, N = 32 / LK;
+  const int part = lane & (LK - 1);
+  const float* sg = a.signs + (it.h % a.table_heads) * D + part * 32;
   const float pre = a.scale * 1.4426950408889634f / sqrtf(static_cast<float>(D));  // logits come in base 2
+  uint32_t neg = 0;  // bit e: sign e is negative
 #pragma unroll
-  for (int e = 0; e < E; ++e) sign[e] = sg[e] * pre;
+  for (int e = 0; e < 32; ++e) neg |= (__ldg(sg + e) < 0.0f ? 1u : 0u) << e;
 #pragma unroll 1
-  for (int r0 = first; r0 < rows; r0 += N * step) {
-    float v[N][E];
+  for (int r0 = first; r0 < last; r0 += step) {
+    const int r = r0 + lane / LK;
+    const int rr = it.m * kRows + min(r, last - 1);  // row of the sequence's (token, group head) list
+    const int64_t off = (it.s.row0 + rr / a.g) * a.q_row + (it.h * a.g + rr % a.g) * a.q_head + part * 32;
+    float v[32];
+    if (a.q_bf16) {
+      const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(a.q) + off;
+      if (a.q_vec) {
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-      const int rr = it.m * kRows + min(r0 + k * step, rows - 1);  // row of the sequence's (token, group head) list
-      const int64_t off = (it.s.row0 + rr / a.g) * a.q_row + (it.h * a.g + rr % a.g) * a.q_head + lane * E;
-      if (a.q_bf16) {
-        const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(a.q) + off;
-        if (a.q_vec) {
-          uint32_t x[E / 2];
-          if constexpr (E == 4) {
-            const uint2 y = *reinterpret_cast<const uint2*>(p);
-            x[0] = y.x; x[1] = y.y;
-          } else {
-            x[0] = *reinterpret_cast<const uint32_t*>(p);
-          }
-#pragma unroll
-          for (int e = 0; e < E; ++e) v[k][e] = e & 1 ? bf16_hi(x[e / 2]) : bf16_lo(x[e / 2]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < E; ++e) v[k][e] = __bfloat162float(p[e]);
+        for (int e = 0; e < 32; e += 8) {
+          const uint4 x = *reinterpret_cast<const uint4*>(p + e);
+          v[e] = bf16_lo(x.x); v[e + 1] = bf16_hi(x.x); v[e + 2] = bf16_lo(x.y); v[e + 3] = bf16_hi(x.y);
+          v[e + 4] = bf16_lo(x.z); v[e + 5] = bf16_hi(x.z); v[e + 6] = bf16_lo(x.w); v[e + 7] = bf16_hi(x.w);
         }
       } else {
-        const float* p = static_cast<const float*>(a.q) + off;
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[k][e] = p[e];
+        for (int e = 0; e < 32; ++e) v[e] = __bfloat162float(p[e]);
       }
-    }
-    float mx[N];
+    } else {
+      const float* p = static_cast<const float*>(a.q) + off;
+      if (a.q_vec) {
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-#pragma unroll
-      for (int e = 0; e < E; ++e) v[k][e] *= sign[e];
-      fwht_warp<E>(v[k], lane);
-      mx[k] = 0.0f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) mx[k] = fmaxf(mx[k], fabsf(v[k][e]));
-    }
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-      const int r = r0 + k * step;
-      const float m = warp_max(mx[k]);
-      // rows whose largest entry lies in [2^-5, 2^14) stay as they are; others are scaled by 2^-ex, 2^ex > m (kept
-      // within 2^-125 .. 2^126, so that it is a normal number)
-      const int ex = (m >= 0x1p-5f && m < 0x1p14f) || m == 0.0f
-                         ? 0 : min(max(static_cast<int>(__float_as_uint(m) >> 23) - 126, -125), 126);
-      const float down = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
-      if (r < rows) {
-        uint32_t h[E / 2];
-#pragma unroll
-        for (int e = 0; e < E; e += 2) h[e / 2] = half2_bits(v[k][e] * down, v[k][e + 1] * down);
-        for (int c = 0; c < reps; ++c) {
-          const int row = r + shift + c * apart;
-          unsigned char* p = qtile + sw128(row, lane * E / 8, kPanel) + (lane * E % 8) * 2;
-          if constexpr (E == 4)
-            *reinterpret_cast<uint2*>(p) = make_uint2(h[0], h[1]);
-          else
-            *reinterpret_cast<uint32_t*>(p) = h[0];
-          if (lane == 0) exps[row] = static_cast<int8_t>(ex);
+        for (int e = 0; e < 32; e += 4) {
+          const float4 x = *reinterpret_cast<const float4*>(p + e);
+          v[e] = x.x; v[e + 1] = x.y; v[e + 2] = x.z; v[e + 3] = x.w;
         }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] = p[e];
       }
+    }
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      v[e] = pre * __uint_as_float(__float_as_uint(v[e]) ^ ((neg << (31 - e)) & 0x80000000u));
+    fwht32_regs(v);
+    fwht32_lanes<LK, 1>(v, lane);
+    float m = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 32; ++e) m = fmaxf(m, fabsf(v[e]));
+#pragma unroll
+    for (int o = 1; o < LK; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    // rows whose largest entry lies in [2^-5, 2^14) stay as they are; others are scaled by 2^-ex, 2^ex > m (kept
+    // within 2^-125 .. 2^126, so that it is a normal number)
+    const int ex = (m >= 0x1p-5f && m < 0x1p14f) || m == 0.0f
+                       ? 0 : min(max(static_cast<int>(__float_as_uint(m) >> 23) - 126, -125), 126);
+    const float down = __uint_as_float(static_cast<uint32_t>(127 - ex) << 23);
+    if (r < last) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint4 h = make_uint4(half2_bits(v[8 * q] * down, v[8 * q + 1] * down),
+                                   half2_bits(v[8 * q + 2] * down, v[8 * q + 3] * down),
+                                   half2_bits(v[8 * q + 4] * down, v[8 * q + 5] * down),
+                                   half2_bits(v[8 * q + 6] * down, v[8 * q + 7] * down));
+        for (int c = 0; c < reps; ++c)
+          *reinterpret_cast<uint4*>(qtile + sw128(r + shift + c * apart, part * 4 + q, kPanel)) = h;
+      }
+      if (part == 0)
+        for (int c = 0; c < reps; ++c) exps[r + shift + c * apart] = static_cast<int8_t>(ex);
     }
   }
 }
@@ -794,10 +792,10 @@ __device__ __forceinline__ bool softmax_role(const AttnArgs& a, const Place& pla
     row.sum = 0.0f;
     if (nt > 0) {
       if (two) {
-        rotate_queries<D>(a, it, sm + Cfg::Q + qt * Cfg::TILE, exps + qt * 128, r0, 1, r0 + wr, -qt * 128, 1, 0, lane);
+        rotate_queries<D>(a, it, sm + Cfg::Q + qt * Cfg::TILE, exps + qt * 128, r0, 1024 / D, r0 + wr, -qt * 128, 1, 0, lane);
         __syncwarp();
       } else {
-        rotate_queries<D>(a, it, sm + Cfg::Q, exps, qt * 4 + warp, 8, rows, 0, reps, apart, lane);
+        rotate_queries<D>(a, it, sm + Cfg::Q, exps, (qt * 4 + warp) * (1024 / D), 8 * (1024 / D), rows, 0, reps, apart, lane);
         named_sync<1, 256>();
       }
       fence_async_shared();
@@ -1255,8 +1253,8 @@ extern "C" int octo_paged_attn(const octo_layout* L, const octo_tables* tab, con
   const size_t ml = (static_cast<size_t>(2) * ctas * a.slot_rows * sizeof(float2) + 255) / 256 * 256;
   a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + ml);
   a.copies = a.part_o + static_cast<size_t>(2) * ctas * a.slot_rows * L->d;
-  const int qe = q_dtype == OCTO_BF16 ? 2 : 4, lane = L->d / 32 * qe;  // bytes of a lane's query values
-  a.q_vec = reinterpret_cast<uintptr_t>(q) % lane == 0 && q_row_stride * qe % lane == 0 && q_head_stride * qe % lane == 0;
+  const int qe = q_dtype == OCTO_BF16 ? 2 : 4;
+  a.q_vec = reinterpret_cast<uintptr_t>(q) % 16 == 0 && q_row_stride * qe % 16 == 0 && q_head_stride * qe % 16 == 0;
   // V comes in boxes that lie inside one page: the largest power of two (8-row swizzle groups) that divides it
   a.box = 16;
   while (a.box < kKeys && pages->page_size % (2 * a.box) == 0) a.box *= 2;

@@ -20,7 +20,6 @@ used on a stream other than the one they were made on need ``record_stream`` as 
 from __future__ import annotations
 
 import ctypes
-import math
 from dataclasses import dataclass
 
 import numpy as np
@@ -28,47 +27,45 @@ import torch
 
 from . import _lib, api
 
-_DTYPES = {torch.float32: _lib.F32, torch.bfloat16: _lib.BF16}
+_F32, _BF16, _I32 = torch.float32, torch.bfloat16, torch.int32
+_DTYPES = {_F32: _lib.F32, _BF16: _lib.BF16}
+_byref = ctypes.byref
+# the current device and stream without the public functions' start-up checks: these calls are a few microseconds of GPU
+# work, and the checks would take longer
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-class _On:
-    """Makes the tensors' device current for a call (and nothing else when it already is), and finds the stream."""
-
-    def __init__(self, device: torch.device, stream):
-        self.guard = None
-        if device.type == "cuda" and device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(device)
-        self.device, self.given = device, stream
-
-    def __enter__(self) -> int:
-        if self.guard is not None:
-            self.guard.__enter__()
-        s = self.given
-        if s is None:
-            if self.device.type != "cuda":
-                raise ValueError(f"the tensors are on {self.device}: a CUDA device is needed")
-            s = torch.cuda.current_stream()
-        elif s.device != self.device:
-            raise ValueError(f"the stream is on {s.device}, the tensors on {self.device}")
-        return int(s.cuda_stream)
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+def _on(index: int, stream, call):
+    """call(stream handle) with the tensors' device current, on ``stream`` or torch's current stream there."""
+    if index < 0:
+        raise ValueError("the tensors must be on a CUDA device")
+    if stream is not None and stream.device_index != index:
+        raise ValueError(f"the stream is on device {stream.device_index}, the tensors on device {index}")
+    if index == _current_device():
+        return call(_raw_stream(index) if stream is None else stream.cuda_stream)
+    with torch.cuda.device(index):
+        return call(_raw_stream(index) if stream is None else stream.cuda_stream)
 
 
-def _same_device(device, *tensors):
+def _same_device(index: int, *tensors):
+    """All tensors are on CUDA device ``index``."""
     for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError(f"a tensor is on device {t.device}, others on device {device}")
+        if t is not None and (index < 0 or t.get_device() != index):
+            dev = {str(x.device) for x in tensors if x is not None}
+            raise ValueError(f"the tensors must be on one CUDA device, they are on device {', '.join(sorted(dev))} "
+                             f"and {index if index >= 0 else 'none'}")
 
 
-def _ints(t: torch.Tensor, what: str, shape) -> torch.Tensor:
-    if t.dtype != torch.int32 or t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
-        raise ValueError(f"{what} must be int32 {['n' if w is None else w for w in shape]}, got {t.dtype} {tuple(t.shape)}")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise ValueError(f"{what} must be contiguous in its last dimension")
-    return t
+def _vector(t: torch.Tensor, what: str, n: int):
+    if t.dtype is not _I32 or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous int32 [{n}], got {t.dtype} {tuple(t.shape)}")
+
+
+def _dense(t: torch.Tensor, what: str, dtype, shape):
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {dtype} {list(shape)} tensor, got {t.dtype} {tuple(t.shape)}")
 
 
 # ------------------------------------------------------------------ rotary positions
@@ -85,23 +82,28 @@ class RopeTable:
         self.theta, self.per_axis = float(theta), bool(per_axis)
         self.c_sections = sec
         self.freqs = torch.from_numpy(f.view(np.int64)).to(device)
+        self.sections_ptr, self.freqs_ptr = sec.ctypes.data, self.freqs.data_ptr()
 
 
-def _rope_tensor(x: torch.Tensor, y: torch.Tensor):
-    return _lib.OctoRopeTensor(x.data_ptr(), y.data_ptr(), x.shape[1], x.stride(0), x.stride(1), y.stride(0), y.stride(1))
+def _end(t: torch.Tensor) -> int:
+    return t.data_ptr() + t.element_size() * (1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride())))
 
 
-def _rope_out(x, out, what):
-    if out is None:
-        return torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    if out.shape != x.shape or out.dtype != x.dtype or (out.stride(-1) != 1 and out.shape[-1] > 1):
-        raise ValueError(f"{what} must have its input's shape and type, contiguous in the last dimension")
-    if out.data_ptr() != x.data_ptr() or out.stride() != x.stride():
-        # the input itself (turned in place) or memory apart from it
-        end = lambda t: t.data_ptr() + t.element_size() * (1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride())))  # noqa: E731
-        if x.numel() and out.data_ptr() < end(x) and x.data_ptr() < end(out):
+def _rope_pair(x: torch.Tensor, y: torch.Tensor | None, what: str):
+    """(output, octo_rope_tensor) of one of rope's tensors."""
+    sx = x.stride()
+    if y is None:
+        y = torch.empty_like(x)
+        sy = y.stride()
+    else:
+        sy = y.stride()
+        if y.shape != x.shape or y.dtype is not x.dtype:
+            raise ValueError(f"{what} must have its input's shape and type")
+        if (y.data_ptr() != x.data_ptr() or sx != sy) and x.numel() and y.data_ptr() < _end(x) and x.data_ptr() < _end(y):
             raise ValueError(f"{what} must be the input itself or not overlap it")
-    return out
+    if (sx[2] != 1 or sy[2] != 1) and x.shape[2] > 1:
+        raise ValueError("rope's tensors must be contiguous in their last dimension")
+    return y, _lib.OctoRopeTensor(x.data_ptr(), y.data_ptr(), x.shape[1], sx[0], sx[1], sy[0], sy[1])
 
 
 def rope(q: torch.Tensor, positions: torch.Tensor, table: RopeTable, k: torch.Tensor | None = None,
@@ -114,25 +116,29 @@ def rope(q: torch.Tensor, positions: torch.Tensor, table: RopeTable, k: torch.Te
     ``inverse`` turns back; as the rotation is orthogonal this is also the gradient: grad_q = rope(grad_out, ...,
     inverse=True). out / k_out may be the inputs (in place). Returns the rotated q, or (q, k).
     """
-    d = q.shape[-1] if q.dim() == 3 else -1
     dt = _DTYPES.get(q.dtype)
-    if d < 0 or dt is None or (q.stride(-1) != 1 and d > 1):
-        raise ValueError(f"q must be float32 or bfloat16 [tokens][heads][d], contiguous in d, got {q.dtype} {tuple(q.shape)}")
-    n = q.shape[0]
-    if k is not None and (k.dim() != 3 or k.shape[0] != n or k.shape[2] != d or k.dtype != q.dtype or
-                          (k.stride(-1) != 1 and d > 1)):
-        raise ValueError(f"k must be {q.dtype} [{n}][heads][{d}], contiguous in d, got {k.dtype} {tuple(k.shape)}")
-    _ints(positions, "positions", (len(table.sections), n))
-    out = _rope_out(q, out, "out")
-    pair = None
+    if dt is None or q.dim() != 3:
+        raise ValueError(f"q must be float32 or bfloat16 [tokens][heads][d], got {q.dtype} {tuple(q.shape)}")
+    n, _, d = q.shape
+    axes = len(table.sections)
+    if positions.dtype is not _I32 or positions.shape != (axes, n) or (n > 1 and positions.stride(1) != 1):
+        raise ValueError(f"positions must be int32 [{axes}][{n}], contiguous in its last dimension, got "
+                         f"{positions.dtype} {tuple(positions.shape)}")
+    out, a = _rope_pair(q, out, "out")
+    b = None
     if k is not None:
-        k_out = _rope_out(k, k_out, "k_out")
-        pair = ctypes.byref(_rope_tensor(k, k_out))
-    _same_device(q.device, k, positions, table.freqs, out, k_out)
-    with _On(q.device, stream) as st:
-        _lib.check(_lib.lib().octo_rope(ctypes.byref(_rope_tensor(q, out)), pair, dt, n, d, positions.data_ptr(),
-                                        max(positions.stride(0), n), len(table.sections), table.c_sections.ctypes.data,
-                                        table.freqs.data_ptr(), int(interleaved), int(inverse), st), "octo_rope")
+        if k.dtype is not q.dtype or k.dim() != 3 or k.shape[0] != n or k.shape[2] != d:
+            raise ValueError(f"k must be {q.dtype} [{n}][heads][{d}], got {k.dtype} {tuple(k.shape)}")
+        k_out, c = _rope_pair(k, k_out, "k_out")
+        b = _byref(c)
+    index = q.get_device()
+    _same_device(index, k, positions, table.freqs, out, k_out)
+    stride = positions.stride(0)
+    st = _on(index, stream, lambda s: _lib.lib().octo_rope(
+        _byref(a), b, dt, n, d, positions.data_ptr(), stride if stride > n else n, axes, table.sections_ptr,
+        table.freqs_ptr, interleaved, inverse, s))
+    if st:
+        _lib.check(st, "octo_rope")
     return out if k is None else (out, k_out)
 
 
@@ -161,9 +167,13 @@ class PagedCache:
             raise ValueError("page_size must be a positive multiple of 16, with at least one page and head")
         if self.status is None:
             self.status = torch.zeros(1, dtype=torch.int32, device=p.device)
-        _same_device(p.device, g, v, self.status)
+        if any(t is not None and t.device != p.device for t in (g, v, self.status)):
+            raise ValueError("the cache's tensors must be on one device")
+        self.shape = (n, h, p.shape[2], s, None if v is None else v.shape[3])  # pages, heads, words, page size, d
+        self.index = p.get_device()
         self.c = _lib.OctoPages(p.data_ptr(), g.data_ptr(), None if v is None else v.data_ptr(), n, h, s,
                                 self.status.data_ptr())
+        self.ref = _byref(self.c)
 
     @classmethod
     def empty(cls, layout: api.Layout, n_pages: int, n_heads: int, page_size: int, values: bool = True, device="cuda"):
@@ -208,18 +218,24 @@ class PagedCache:
 
 
 def _check_pool(layout: api.Layout, cache: PagedCache, values: bool):
-    if cache.packed.shape[2] != layout.words:
-        raise ValueError(f"the cache holds {cache.packed.shape[2]} words per key, {layout!r} has {layout.words}")
-    if cache.V is None:
+    c = layout.c
+    if cache.shape[2] != c.words:
+        raise ValueError(f"the cache holds {cache.shape[2]} words per key, {layout!r} has {c.words}")
+    if cache.shape[4] is None:
         if values:
             raise ValueError("the cache holds no values")
-    elif cache.V.shape[3] != layout.d:
-        raise ValueError(f"the cache's V rows have {cache.V.shape[3]} elements, {layout!r} has d={layout.d}")
+    elif cache.shape[4] != c.d:
+        raise ValueError(f"the cache's V rows have {cache.shape[4]} elements, {layout!r} has d={c.d}")
 
 
-def _table(page_table: torch.Tensor, B: int):
-    _ints(page_table, "page_table", (B, None))
-    return _lib.OctoPageTable(page_table.data_ptr(), max(page_table.stride(0), page_table.shape[1]), B, page_table.shape[1])
+def _table(page_table: torch.Tensor, B: int, what: str = "page_table"):
+    if page_table.dtype is not _I32 or page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError(f"{what} must be int32 [{B}][pages], got {page_table.dtype} {tuple(page_table.shape)}")
+    n = page_table.shape[1]
+    s0, s1 = page_table.stride()
+    if s1 != 1 and n > 1:
+        raise ValueError(f"{what} must be contiguous in its last dimension")
+    return _lib.OctoPageTable(page_table.data_ptr(), s0 if s0 > n else n, B, n)
 
 
 def paged_write(layout: api.Layout, staged: api.Cache, V: torch.Tensor | None, cache: PagedCache,
@@ -231,34 +247,32 @@ def paged_write(layout: api.Layout, staged: api.Cache, V: torch.Tensor | None, c
     for a cache without values; starts int32 [B], cu int32 [B + 1]. No two tokens may go to one slot.
     """
     _check_pool(layout, cache, False)
-    B = int(starts.shape[0])
-    _ints(starts, "starts", (B,))
-    _ints(cu, "cu", (B + 1,))
-    H = cache.n_heads
+    B, H, W, d = starts.numel(), cache.shape[1], cache.shape[2], layout.c.d
+    _vector(starts, "starts", B)
+    _vector(cu, "cu", B + 1)
+    if (V is None) != (cache.V is None):
+        raise ValueError("the cache holds values: V is needed" if V is None else "the cache holds no values")
     if V is None:
-        if cache.V is not None:
-            raise ValueError("the cache holds values: V is needed")
-        rows = staged.length
-        vs = (0, 0)
+        rows, sr, sh, pv = staged.length, 0, 0, None
     else:
-        if cache.V is None:
-            raise ValueError("the cache holds no values")
-        if V.dtype != torch.bfloat16 or V.dim() != 3 or V.shape[1] != H or V.shape[2] != layout.d or V.stride(2) != 1:
-            raise ValueError(f"V must be bfloat16 [rows][{H}][{layout.d}], contiguous in its last dimension")
-        rows, vs = int(V.shape[0]), (V.stride(0), V.stride(1))
-        if vs[0] % 8 or vs[1] % 8 or V.data_ptr() % 16:
+        if V.dtype is not _BF16 or V.dim() != 3 or V.shape[1] != H or V.shape[2] != d or V.stride(2) != 1:
+            raise ValueError(f"V must be bfloat16 [rows][{H}][{d}], contiguous in its last dimension")
+        rows, sr, sh, pv = V.shape[0], V.stride(0), V.stride(1), V.data_ptr()
+        if sr % 8 or sh % 8 or pv % 16:
             raise ValueError("V rows must start on 16-byte boundaries")
-    p = staged.packed
-    if (p.dtype != torch.int32 or p.dim() != 3 or p.shape[0] != H or p.shape[1] != layout.words or p.shape[2] < rows or
-            not p.is_contiguous() or staged.gamma.dtype != torch.float32 or
-            tuple(staged.gamma.shape) != (H, p.shape[2]) or not staged.gamma.is_contiguous()):
+    p, g = staged.packed, staged.gamma
+    cap = p.shape[-1]
+    if p.dtype is not _I32 or p.shape != (H, W, cap) or cap < rows or not p.is_contiguous():
         raise ValueError(f"staged must hold {H} heads of {layout!r} with at least {rows} tokens")
-    _same_device(cache.packed.device, p, staged.gamma, V, page_table, starts, cu)
-    with _On(cache.packed.device, stream) as st:
-        _lib.check(_lib.lib().octo_paged_write(layout.ref, ctypes.byref(cache.c), ctypes.byref(_table(page_table, B)),
-                                               p.data_ptr(), staged.gamma.data_ptr(), p.shape[2],
-                                               None if V is None else V.data_ptr(), vs[0], vs[1], rows, starts.data_ptr(),
-                                               cu.data_ptr(), st), "octo_paged_write")
+    _dense(g, "staged.gamma", _F32, (H, cap))
+    t = _table(page_table, B)
+    index = cache.index
+    _same_device(index, p, g, V, page_table, starts, cu)
+    st = _on(index, stream, lambda s: _lib.lib().octo_paged_write(
+        layout.ref, cache.ref, _byref(t), p.data_ptr(), g.data_ptr(), cap, pv, sr, sh, rows, starts.data_ptr(),
+        cu.data_ptr(), s))
+    if st:
+        _lib.check(st, "octo_paged_write")
     return cache
 
 
@@ -274,31 +288,32 @@ def paged_append(layout: api.Layout, tables: api.DeviceTables, keys: torch.Tenso
         raise ValueError(f"V holds {V.shape[0]} rows, keys {rows}")
     if staged is None:
         staged = api.Cache.empty(layout, cache.n_heads, max(rows, 1), device=keys.device)
-    with _On(keys.device, stream):
-        api.encode(layout, tables, keys.transpose(0, 1), staged, 0, stream=stream)
+    rows_of = keys.transpose(0, 1)
+    _on(keys.get_device(), stream, lambda s: api.encode(layout, tables, rows_of, staged, 0, stream=stream))
     staged.length = rows
     return paged_write(layout, staged, V, cache, page_table, starts, cu, stream=stream)
 
 
-def _chunk(layout, tables, q, cache, page_table, seq_lens, cu_q, extra):
-    """Checks of the calls that take a chunk of queries; returns (dtype, rows, Hq, B, cu_q)."""
-    if q.dim() != 3 or q.shape[2] != layout.d or (q.stride(2) != 1 and layout.d > 1):
-        raise ValueError(f"q must be [rows][heads][{layout.d}], contiguous in its last dimension, got {tuple(q.shape)}")
+def _chunk(layout, tables, q, cache, page_table, seq_lens, cu_q):
+    """Checks of the calls that take a chunk of queries; returns (dtype, rows, Hq, B, cu_q, octo_page_table)."""
+    d, H = layout.c.d, cache.shape[1]
     dt = _DTYPES.get(q.dtype)
     if dt is None:
         raise ValueError(f"unsupported query dtype {q.dtype}")
-    rows, Hq, H = int(q.shape[0]), int(q.shape[1]), cache.n_heads
+    if q.dim() != 3 or q.shape[2] != d or q.stride(2) != 1:
+        raise ValueError(f"q must be [rows][heads][{d}], contiguous in its last dimension, got {tuple(q.shape)}")
+    rows, Hq, _ = q.shape
     if Hq < H or Hq % H:
         raise ValueError(f"{Hq} query heads over {H} cache heads")
-    B = int(seq_lens.shape[0])
-    _ints(seq_lens, "seq_lens", (B,))
+    B = seq_lens.numel()
+    _vector(seq_lens, "seq_lens", B)
     if cu_q is None:
         if B == 0 or rows % B:
             raise ValueError(f"{rows} query rows over {B} sequences: cu_q is needed")
-        cu_q = torch.arange(B + 1, dtype=torch.int32, device=q.device) * (rows // B)
-    _ints(cu_q, "cu_q", (B + 1,))
-    _same_device(cache.packed.device, q, page_table, seq_lens, cu_q, tables.dir_c, tables.rho_c, tables.signs, *extra)
-    return dt, rows, Hq, B, cu_q
+        cu_q = torch.arange(B + 1, dtype=_I32, device=q.device) * (rows // B)
+    _vector(cu_q, "cu_q", B + 1)
+    _same_device(cache.index, q, page_table, seq_lens, cu_q, tables.dir_c, tables.signs)
+    return dt, rows, Hq, B, cu_q, _table(page_table, B)
 
 
 def paged_attn_workspace_bytes(layout: api.Layout, rows: int, B: int, Hq: int, Hkv: int) -> int:
@@ -309,14 +324,15 @@ def paged_mass_workspace_bytes(layout: api.Layout, rows: int, B: int, Hq: int, H
     return int(_lib.lib().octo_paged_mass_workspace(layout.ref, rows, B, Hq, Hkv))
 
 
-def _workspace(workspace, need, device):
+def _scratch(workspace, need: int, cache: PagedCache):
+    """A device buffer of ``need`` bytes: the workspace's, or one for this call."""
     if workspace is None:
-        workspace = torch.empty((need + 255) // 256 * 64, dtype=torch.int32, device=device)
-        return workspace, workspace.data_ptr(), workspace.numel() * 4
-    if workspace.buf.device != device:
-        raise ValueError(f"the workspace is on {workspace.buf.device}, the cache on {device}")
-    workspace.ensure(need)
-    return workspace, workspace.buf.data_ptr(), workspace.nbytes
+        return torch.empty((need + 255) // 256 * 64, dtype=_I32, device=cache.packed.device)
+    if workspace.buf.get_device() != cache.index:
+        raise ValueError(f"the workspace is on {workspace.buf.device}, the cache on {cache.packed.device}")
+    if need > workspace.buf.numel() * 4:
+        workspace.ensure(need)
+    return workspace.buf
 
 
 def paged_attn(layout: api.Layout, tables: api.DeviceTables, q: torch.Tensor, cache: PagedCache, page_table: torch.Tensor,
@@ -341,22 +357,26 @@ def paged_attn(layout: api.Layout, tables: api.DeviceTables, q: torch.Tensor, ca
     if odt is None:
         raise ValueError(f"unsupported output dtype {out.dtype}")
     if lse is True:
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+        lse = torch.empty(q.shape[:2], dtype=_F32, device=q.device)
     elif lse is False:
         lse = None
-    elif lse is not None and (lse.dtype != torch.float32 or lse.shape != q.shape[:2] or not lse.is_contiguous()):
-        raise ValueError(f"lse must be a contiguous float32 {tuple(q.shape[:2])} tensor")
+    elif lse is not None:
+        _dense(lse, "lse", _F32, q.shape[:2])
     _check_pool(layout, cache, True)
-    dt, rows, Hq, B, cu_q = _chunk(layout, tables, q, cache, page_table, seq_lens, cu_q, (out, lse))
-    lib = _lib.lib()
-    with _On(q.device, stream) as st:
-        need = lib.octo_paged_attn_workspace(layout.ref, rows, B, Hq, cache.n_heads)
-        hold, ws, nbytes = _workspace(workspace, need, q.device)
-        _lib.check(lib.octo_paged_attn(layout.ref, tables.ref, ctypes.byref(cache.c), ctypes.byref(_table(page_table, B)),
-                                       seq_lens.data_ptr(), q.data_ptr(), dt, q.stride(0), q.stride(1), rows, Hq,
-                                       cu_q.data_ptr(), int(causal), 1.0 / math.sqrt(layout.d) if scale is None else scale,
-                                       out.data_ptr(), odt, None if lse is None else lse.data_ptr(), ws, nbytes, st),
-                   "octo_paged_attn")
+    dt, rows, Hq, B, cu_q, t = _chunk(layout, tables, q, cache, page_table, seq_lens, cu_q)
+    index, lib = cache.index, _lib.lib()
+    _same_device(index, out, lse)
+
+    def call(s):
+        ws = _scratch(workspace, lib.octo_paged_attn_workspace(layout.ref, rows, B, Hq, cache.shape[1]), cache)
+        return lib.octo_paged_attn(
+            layout.ref, tables.ref, cache.ref, _byref(t), seq_lens.data_ptr(), q.data_ptr(), dt, q.stride(0), q.stride(1),
+            rows, Hq, cu_q.data_ptr(), causal, layout.c.d ** -0.5 if scale is None else scale, out.data_ptr(), odt,
+            None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel() * 4, s)
+
+    st = _on(index, stream, call)
+    if st:
+        _lib.check(st, "octo_paged_attn")
     return out if lse is None else (out, lse)
 
 
@@ -368,29 +388,31 @@ def paged_mass(layout: api.Layout, tables: api.DeviceTables, q: torch.Tensor, ls
     sum over the chunk's rows and the cache head's query heads of exp(scale * logit_j - lse), for slots j < seq_lens[i];
     later slots of out are left as they were. q, masks and lse (float32 [rows][Hq]) as in :func:`paged_attn`; mass
     float32 [B][heads][slots]; out is mass itself (in place) by default."""
-    H = cache.n_heads
+    B, H = seq_lens.numel(), cache.shape[1]
+    slots = mass.shape[-1]
+    _dense(mass, "mass", _F32, (B, H, slots))
     if out is None:
         out = mass
-    for t, what in ((mass, "mass"), (out, "out")):
-        if t.dtype != torch.float32 or t.dim() != 3 or tuple(t.shape[:2]) != (seq_lens.shape[0], H) or not t.is_contiguous():
-            raise ValueError(f"{what} must be a contiguous float32 [{seq_lens.shape[0]}][{H}][slots] tensor")
-    if out.shape != mass.shape:
-        raise ValueError(f"out must be {tuple(mass.shape)} as mass is")
-    if out.data_ptr() != mass.data_ptr() and abs(out.data_ptr() - mass.data_ptr()) < 4 * mass.numel():
-        raise ValueError("out must be mass itself or not overlap it")
-    if lse.dtype != torch.float32 or tuple(lse.shape) != tuple(q.shape[:2]) or not lse.is_contiguous():
-        raise ValueError(f"lse must be a contiguous float32 {tuple(q.shape[:2])} tensor")
+    elif out is not mass:
+        _dense(out, "out", _F32, (B, H, slots))
+        if out.data_ptr() != mass.data_ptr() and abs(out.data_ptr() - mass.data_ptr()) < 4 * mass.numel():
+            raise ValueError("out must be mass itself or not overlap it")
+    _dense(lse, "lse", _F32, q.shape[:2])
     _check_pool(layout, cache, False)
-    dt, rows, Hq, B, cu_q = _chunk(layout, tables, q, cache, page_table, seq_lens, cu_q, (lse, mass, out))
-    lib = _lib.lib()
-    with _On(q.device, stream) as st:
-        need = lib.octo_paged_mass_workspace(layout.ref, rows, B, Hq, H)
-        hold, ws, nbytes = _workspace(workspace, need, q.device)
-        _lib.check(lib.octo_paged_mass(layout.ref, tables.ref, ctypes.byref(cache.c), ctypes.byref(_table(page_table, B)),
-                                       seq_lens.data_ptr(), q.data_ptr(), dt, q.stride(0), q.stride(1), rows, Hq,
-                                       cu_q.data_ptr(), int(causal), 1.0 / math.sqrt(layout.d) if scale is None else scale,
-                                       lse.data_ptr(), decay, mass.data_ptr(), out.data_ptr(), mass.shape[2], ws, nbytes,
-                                       st), "octo_paged_mass")
+    dt, rows, Hq, B, cu_q, t = _chunk(layout, tables, q, cache, page_table, seq_lens, cu_q)
+    index, lib = cache.index, _lib.lib()
+    _same_device(index, lse, mass, out)
+
+    def call(s):
+        ws = _scratch(workspace, lib.octo_paged_mass_workspace(layout.ref, rows, B, Hq, H), cache)
+        return lib.octo_paged_mass(
+            layout.ref, tables.ref, cache.ref, _byref(t), seq_lens.data_ptr(), q.data_ptr(), dt, q.stride(0), q.stride(1),
+            rows, Hq, cu_q.data_ptr(), causal, layout.c.d ** -0.5 if scale is None else scale, lse.data_ptr(), decay,
+            mass.data_ptr(), out.data_ptr(), slots, ws.data_ptr(), ws.numel() * 4, s)
+
+    st = _on(index, stream, call)
+    if st:
+        _lib.check(st, "octo_paged_mass")
     return out
 
 
@@ -406,31 +428,34 @@ def paged_evict(layout: api.Layout, cache: PagedCache, page_table: torch.Tensor,
     Returns (new_lens int32 [B], kept int32 [B][heads][keep]: the slots kept, -1 behind the last; new_mass float32
     [B][heads][keep], 0 behind the last). Kept tokens keep the positions that their keys were rotated by.
     """
-    dst = cache if dst is None else dst
     _check_pool(layout, cache, False)
-    _check_pool(layout, dst, False)
-    B, H, keep = int(seq_lens.shape[0]), cache.n_heads, int(keep)
-    _ints(seq_lens, "seq_lens", (B,))
-    if mass.dtype != torch.float32 or mass.dim() != 3 or tuple(mass.shape[:2]) != (B, H) or not mass.is_contiguous():
-        raise ValueError(f"mass must be a contiguous float32 [{B}][{H}][slots] tensor")
+    if dst is None:
+        dst = cache
+    else:
+        _check_pool(layout, dst, False)
+    B, H, slots = seq_lens.numel(), cache.shape[1], mass.shape[-1]
+    _vector(seq_lens, "seq_lens", B)
+    _dense(mass, "mass", _F32, (B, H, slots))
     if keep < 1:
         raise ValueError(f"keep must be at least 1, got {keep}")
-    dev = cache.packed.device
+    dev, index = mass.device, cache.index
     if kept is None:
-        kept = torch.empty((B, H, keep), dtype=torch.int32, device=dev)
+        kept = torch.empty((B, H, keep), dtype=_I32, device=dev)
+    else:
+        _dense(kept, "kept", _I32, (B, H, keep))
     if new_lens is None:
-        new_lens = torch.empty((B,), dtype=torch.int32, device=dev)
+        new_lens = torch.empty((B,), dtype=_I32, device=dev)
+    else:
+        _vector(new_lens, "new_lens", B)
     if new_mass is None:
-        new_mass = torch.empty((B, H, keep), dtype=torch.float32, device=dev)
-    for t, what, shape, ty in ((kept, "kept", (B, H, keep), torch.int32), (new_lens, "new_lens", (B,), torch.int32),
-                               (new_mass, "new_mass", (B, H, keep), torch.float32)):
-        if t.dtype != ty or tuple(t.shape) != shape or not t.is_contiguous():
-            raise ValueError(f"{what} must be a contiguous {ty} {shape} tensor")
-    _same_device(dev, page_table, seq_lens, mass, dst_table, dst.packed, kept, new_lens, new_mass)
-    with _On(dev, stream) as st:
-        _lib.check(_lib.lib().octo_paged_evict(layout.ref, ctypes.byref(cache.c), ctypes.byref(_table(page_table, B)),
-                                               seq_lens.data_ptr(), mass.data_ptr(), mass.shape[2], keep, int(sink),
-                                               int(recent), ctypes.byref(dst.c), ctypes.byref(_table(dst_table, B)),
-                                               kept.data_ptr(), new_lens.data_ptr(), new_mass.data_ptr(), st),
-                   "octo_paged_evict")
+        new_mass = torch.empty((B, H, keep), dtype=_F32, device=dev)
+    else:
+        _dense(new_mass, "new_mass", _F32, (B, H, keep))
+    t, z = _table(page_table, B), _table(dst_table, B, "dst_table")
+    _same_device(index, page_table, seq_lens, mass, dst_table, dst.packed, kept, new_lens, new_mass)
+    st = _on(index, stream, lambda s: _lib.lib().octo_paged_evict(
+        layout.ref, cache.ref, _byref(t), seq_lens.data_ptr(), mass.data_ptr(), slots, keep, sink, recent, dst.ref,
+        _byref(z), kept.data_ptr(), new_lens.data_ptr(), new_mass.data_ptr(), s))
+    if st:
+        _lib.check(st, "octo_paged_evict")
     return new_lens, kept, new_mass
