@@ -126,6 +126,7 @@ __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
 // Waits for the phase of this parity; false when it did not end within the
 // limit (about a second of polls), and then the caller gives up.
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
+#pragma unroll 1
   for (int it = 0; it < (1 << 22); ++it) {
     uint32_t ok;
     asm volatile(

@@ -47,8 +47,15 @@ namespace paged {
 
 constexpr int kRows = 256;   // query rows of an item
 constexpr int kKeys = 128;   // slots of a key tile
-constexpr int kJoin = 256;   // CTAs that may share an item: the launch has no more
+constexpr int kJoin = 148;    // CTAs that may share an item: the launch has no more
+constexpr int kJoinRows = 4;  // rows of a block of the join
 constexpr int kPanel = 128 * 128;  // bytes of a 128-row panel of 64 halves
+
+// An item that a CTA begins and others go on with, as the join finds it: its
+// rows, and the number of CTAs that hold a piece (0: the CTA begins no such item).
+struct Shared {
+  int pieces, rows, copies, row0, h, m, pad[2];  // copies: row copies in each piece
+};
 
 struct AttnArgs {
   Table t;
@@ -67,10 +74,10 @@ struct AttnArgs {
   void* out;
   int out_bf16;
   float* lse;
-  float* part_o;   // [slots][slot_rows][D]
-  float* copies;   // [CTAs][256][D]: the row copies of an item of at most 128 rows, on their way to their sum
-  float2* part_ml; // [slots][slot_rows]
-  int slot_rows;
+  float4* part_o;  // [slots][D / 4][256]: lanes own rows, so their accesses are contiguous
+  float4* copies;  // [CTAs][D / 4][256]: the row copies of an item of at most 128 rows, on their way to their sum
+  float2* part_ml; // [slots][256]
+  Shared* shared;  // [CTAs]
 };
 
 // An item's place: sequence, head, 256-row tile, and its key tiles.
@@ -95,7 +102,7 @@ __device__ __forceinline__ int64_t head_tiles(const Seq& s, int g, int causal) {
 
 // Where a CTA's piece of the list starts (warp-wide, all lanes the same).
 struct Place {
-  int64_t count;  // key tiles of the piece
+  int64_t start, count, total;  // the piece's first key tile in the list and their number; tiles of the list
   int i, h, m, tile;
 };
 __device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {
@@ -117,9 +124,10 @@ __device__ int64_t total_tiles(const AttnArgs& a, int lane, bool tell) {
 __device__ Place find_place(const AttnArgs& a, int lane, int64_t total) {
   // no more pieces than tiles: an empty piece would leave no partial where the join looks for one
   const int64_t ctas = min(static_cast<int64_t>(gridDim.x), total);
-  Place p{0, 0, 0, 0, 0};
+  Place p{0, 0, total, 0, 0, 0, 0};
   if (blockIdx.x >= ctas) return p;
   const int64_t at = blockIdx.x * total / ctas;
+  p.start = at;
   p.count = (blockIdx.x + 1) * total / ctas - at;
   int64_t before = 0;
   for (int base = 0; base < a.t.n_seqs; base += 32) {
@@ -223,7 +231,7 @@ struct AttnCfg {
   static constexpr int Q = 0, KT = 2 * TILE, V = 4 * TILE, TAB = 6 * TILE, RHO = TAB + (NE << SH);
   static constexpr int GAM = RHO + (QUAD ? 8 * 8 * 4 : 0), GMAX = GAM + GS * kKeys * 4, EXPS = GMAX + GS * 16,
                        BARS = EXPS + 256;
-  static constexpr int PLACE = BARS + 144, TMEM = PLACE + 40, DIR = PLACE + 64, RHOF = DIR + 128, SMEM = RHOF + 32;
+  static constexpr int PLACE = BARS + 144, TMEM = PLACE + 40, DIR = PLACE + 48, RHOF = DIR + 128, SMEM = RHOF + 32;
   static_assert(SMEM <= 232448, "shared memory of an SM");
   static constexpr int THREADS = 512;
 };
@@ -838,22 +846,43 @@ __device__ __forceinline__ bool softmax_role(const AttnArgs& a, const Place& pla
     c += nt;
     // ---- results of the item (or of this piece of it)
     const bool whole = it.t0 == 0 && it.t1 == it.tiles;
-    const int64_t prow = (2 * static_cast<int64_t>(blockIdx.x) + (it.t0 > 0 ? 0 : 1)) * a.slot_rows;
+    if (!whole && it.t0 == 0 && (threadIdx.x & 255) == 0) {
+      // the item's last tile lies with the last CTA whose piece starts at or before it
+      const int64_t last = place.start + (place.count - it.left) + it.tiles - 1;
+      const int64_t ctas = min(static_cast<int64_t>(gridDim.x), place.total);
+      const int to = static_cast<int>(((last + 1) * ctas + place.total - 1) / place.total - 1);
+      a.shared[blockIdx.x] = Shared{to - static_cast<int>(blockIdx.x) + 1, rows, two ? 1 : 2 * reps, it.s.row0, it.h, it.m, {0, 0}};
+    }
+    const int64_t slot = 2 * static_cast<int64_t>(blockIdx.x) + (it.t0 > 0 ? 0 : 1);
     const int64_t row_at = static_cast<int64_t>(it.s.row0) * a.Hq + static_cast<int64_t>(it.h) * a.g;
     auto out_row = [&](int y) {  // row y of the item in out and lse
       const int q = it.m * kRows + y;
       return row_at + static_cast<int64_t>(q / a.g) * a.Hq + q % a.g;
     };
-    if (two || nt == 0) {
-      if (wr > 0 && (two || qt == 0) && (two || warp * 32 < apart)) {
-        const float sum = row.sum, inv = whole ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f;
-        const int64_t orow = out_row(x);
-        if (there) {
-          if (!whole)
-            a.part_ml[prow + x] = make_float2(row.ref, sum);
-          else if (a.lse)
-            a.lse[orow] = sum == 0.0f ? -INFINITY : (row.ref + log2f(sum)) * 0.6931471805599453f;
+    if (!whole) {
+      // rows, or row copies, for the join
+      if (there) a.part_ml[slot * 256 + qt * 128 + warp * 32 + lane] = make_float2(row.ref, row.sum);
+      if (wr > 0) {
+        float4* dst = a.part_o + slot * (D / 4) * 256 + qt * 128 + warp * 32 + lane;
+#pragma unroll 1
+        for (int k = 0; k < D; k += 16) {
+          uint32_t o[16];
+          tmem_ld16(o, row.O + k);
+          tc_wait_ld();
+          if (there) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y)  // (a row without a slot here may find anything in O)
+              dst[(k / 4 + y) * 256] = row.sum == 0.0f ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
+                                                       : make_float4(__uint_as_float(o[4 * y]), __uint_as_float(o[4 * y + 1]),
+                                                                     __uint_as_float(o[4 * y + 2]), __uint_as_float(o[4 * y + 3]));
+          }
         }
+      }
+    } else if (two || nt == 0) {
+      if (wr > 0 && (two || qt == 0) && (two || warp * 32 < apart)) {
+        const float sum = row.sum, inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const int64_t orow = out_row(x);
+        if (there && a.lse) a.lse[orow] = sum == 0.0f ? -INFINITY : (row.ref + log2f(sum)) * 0.6931471805599453f;
 #pragma unroll 1
         for (int k = 0; k < D; k += 32) {
           uint32_t o[32];
@@ -865,15 +894,7 @@ __device__ __forceinline__ bool softmax_role(const AttnArgs& a, const Place& pla
           // a row that saw nothing gives 0
 #pragma unroll
           for (int y = 0; y < 32; ++y) v[y] = nt == 0 || sum == 0.0f ? 0.0f : __uint_as_float(o[y]) * inv;
-          if (there) {
-            if (whole) {
-              store32(a, orow * D + k, v);
-            } else {
-              float4* dst = reinterpret_cast<float4*>(a.part_o + (prow + x) * D + k);
-#pragma unroll
-              for (int y = 0; y < 32; y += 4) dst[y / 4] = make_float4(v[y], v[y + 1], v[y + 2], v[y + 3]);
-            }
-          }
+          if (there) store32(a, orow * D + k, v);
         }
       }
     } else {
@@ -891,52 +912,47 @@ __device__ __forceinline__ bool softmax_role(const AttnArgs& a, const Place& pla
         all = fmaf(ex2(y.x - base), y.y, all);
       }
       if (qt == 0 && warp * 32 < apart) ml[256 + x] = make_float2(top, all);
-      float* mine = a.copies + (static_cast<int64_t>(blockIdx.x) * 256 + me) * D;
+      float4* mine = a.copies + static_cast<int64_t>(blockIdx.x) * (D / 4) * 256;
       if (wr > 0) {
         const float keep = row.sum == 0.0f ? 0.0f : ex2(row.ref - base);
 #pragma unroll 1
-        for (int k = 0; k < D; k += 32) {
-          uint32_t o[32];
-          tmem_ld32(o, row.O + k);
+        for (int k = 0; k < D; k += 16) {
+          uint32_t o[16];
+          tmem_ld16(o, row.O + k);
           tc_wait_ld();
           if (there) {
 #pragma unroll
-            for (int y = 0; y < 32; y += 4) {
-              float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-              if (row.sum != 0.0f)  // a copy without a slot may hold anything
-                v = make_float4(__uint_as_float(o[y]) * keep, __uint_as_float(o[y + 1]) * keep,
-                                __uint_as_float(o[y + 2]) * keep, __uint_as_float(o[y + 3]) * keep);
-              *reinterpret_cast<float4*>(mine + k + y) = v;
-            }
+            for (int y = 0; y < 4; ++y)  // a copy without a slot may hold anything
+              mine[(k / 4 + y) * 256 + me] =
+                  row.sum == 0.0f ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
+                                  : make_float4(__uint_as_float(o[4 * y]) * keep, __uint_as_float(o[4 * y + 1]) * keep,
+                                                __uint_as_float(o[4 * y + 2]) * keep, __uint_as_float(o[4 * y + 3]) * keep);
           }
         }
       }
       named_sync<1, 256>();
-      const int tid = threadIdx.x & 255;
-      for (int e = tid; e < rows * (D / 4); e += 256) {
-        const int y = e / (D / 4), d = e % (D / 4) * 4;
+      // threads along four rows, so that reads and writes both meet in sectors
+      const int tid = threadIdx.x & 255, y0 = tid & 3;
+      for (int e = tid >> 2; e < (rows + 3) / 4 * (D / 4); e += 64) {
+        const int y = e / (D / 4) * 4 + y0, d = e % (D / 4);
+        if (y >= rows) continue;
         const float2 t = ml[256 + y];
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        const float* src = a.copies + (static_cast<int64_t>(blockIdx.x) * 256 + y) * D + d;
+        const float4* src = mine + d * 256 + y;
+#pragma unroll 2
         for (int k = 0; k < 2 * reps; ++k) {
-          const float4 v = *reinterpret_cast<const float4*>(src + static_cast<int64_t>((k & 1) * 128 + (k >> 1) * apart) * D);
+          const float4 v = src[(k & 1) * 128 + (k >> 1) * apart];
           o.x += v.x; o.y += v.y; o.z += v.z; o.w += v.w;
         }
-        if (whole) {
-          const int64_t orow = out_row(y);
-          const float inv = t.y == 0.0f ? 0.0f : 1.0f / t.y;
-          if (a.out_bf16) {
-            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + orow * D + d) =
-                make_uint2(bf16_pair(o.x * inv, o.y * inv), bf16_pair(o.z * inv, o.w * inv));
-          } else {
-            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + orow * D + d) =
-                make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-          }
-          if (a.lse && d == 0) a.lse[orow] = t.y == 0.0f ? -INFINITY : (t.x + log2f(t.y)) * 0.6931471805599453f;
-        } else {
-          *reinterpret_cast<float4*>(a.part_o + (prow + y) * D + d) = o;
-          if (d == 0) a.part_ml[prow + y] = t;
-        }
+        const int64_t orow = out_row(y);
+        const float inv = t.y == 0.0f ? 0.0f : 1.0f / t.y;
+        if (a.out_bf16)
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + orow * D + 4 * d) =
+              make_uint2(bf16_pair(o.x * inv, o.y * inv), bf16_pair(o.z * inv, o.w * inv));
+        else
+          *reinterpret_cast<float4*>(static_cast<float*>(a.out) + orow * D + 4 * d) =
+              make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+        if (a.lse && d == 0) a.lse[orow] = t.y == 0.0f ? -INFINITY : (t.x + log2f(t.y)) * 0.6931471805599453f;
       }
       named_sync<1, 256>();
     }
@@ -960,11 +976,6 @@ __global__ void __launch_bounds__(512, 1) paged_attn_kernel(const __grid_constan
   float* s_rho = reinterpret_cast<float*>(sm + Cfg::RHOF);
   if (tid < (1 << (B + 1))) s_dir[tid] = a.dir_c[tid];
   if (tid < K::NRHO) s_rho[tid] = a.rho_c[tid];
-  if (warp == 15) {
-    const int64_t total = total_tiles(a, lane, blockIdx.x == 0);
-    const Place p = find_place(a, lane, total);
-    if (lane == 0) s_place = p;
-  }
   if (tid == 0) {
     for (int q = 0; q < 2; ++q) {
       bar_init(bars + 8 * (kQF + q), 128);
@@ -980,11 +991,15 @@ __global__ void __launch_bounds__(512, 1) paged_attn_kernel(const __grid_constan
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 12) tmem_alloc(s32(&s_tmem), 512);
+  if (tid == 32) a.shared[blockIdx.x].pieces = 0;
   __syncthreads();
-  const Place place = s_place;
-  if (place.count > 0) {
+  if (warp == 15) {
+    const int64_t total = total_tiles(a, lane, blockIdx.x == 0);
+    const Place p = find_place(a, lane, total);
+    if (lane == 0) s_place = p;
+  } else {
     // decoded codes (b = 4: directions) in fp16, and their copies
-    for (int e = tid; e < Cfg::NE; e += Cfg::THREADS) {
+    for (int e = tid; e < Cfg::NE; e += 480) {
       const int field = Cfg::QUAD ? e & ((1 << 2 * B) - 1) : e & (K::NDIR - 1);
       const float3 d = field_direction<B>(field, s_dir);
       const float r = Cfg::QUAD ? 1.0f : s_rho[(e >> K::DIR) & (K::NRHO - 1)];
@@ -999,6 +1014,7 @@ __global__ void __launch_bounds__(512, 1) paged_attn_kernel(const __grid_constan
   tc_before();
   __syncthreads();
   tc_after();
+  const Place place = s_place;
   constexpr uint32_t tmem = 0;  // the allocation is the whole tensor memory, so it starts at column 0
   bool ok = true;
   if (place.count > 0) {
@@ -1030,108 +1046,91 @@ __global__ void __launch_bounds__(512, 1) paged_attn_kernel(const __grid_constan
 }
 
 // ---- joining the pieces of shared items --------------------------------------
-// One block per (256-row tile of any sequence, head, 32 rows of the tile); it
-// finds the item's place in the list as the CTAs of the first kernel did.
+// One block per (CTA that begins an item others go on with, 4 rows of it). A
+// row's entries are its copies in each piece.
 template <int D>
-__global__ void __launch_bounds__(256) paged_attn_join(const __grid_constant__ AttnArgs a, int grid_ctas) {
-  const int h = blockIdx.y, tid = threadIdx.x, lane = tid & 31, r0 = blockIdx.z * 32;
-  __shared__ int64_t s_at, s_total;
-  __shared__ int s_i, s_m;
-  if (tid < 32) {
-    int64_t items = 0, before = 0;  // row tiles of the sequences so far; their key tiles
-    int who = -1, mine = 0;
-    int64_t at = 0;
-    for (int base = 0; base < a.t.n_seqs; base += 32) {
-      const int i = base + lane;
-      Seq s{0, 0, 0};
-      if (i < a.t.n_seqs) s = seq_of(a.t, a.seq_lens, a.cu, a.n_rows, i);
-      const int64_t mt = row_tiles(s, a.g), n = mt ? head_tiles(s, a.g, a.causal) * a.t.n_heads : 0;
-      const int64_t mend = items + warp_scan(mt, lane), nend = before + warp_scan(n, lane);
-      const bool hit = static_cast<int64_t>(blockIdx.x) < mend && static_cast<int64_t>(blockIdx.x) >= mend - mt;
-      if (hit) {
-        who = i;
-        mine = static_cast<int>(blockIdx.x - (mend - mt));
-        at = nend - n + h * (n / a.t.n_heads);
-        for (int k = 0; k < mine; ++k) at += item_tiles(s, a.g, a.causal, k);
-        s_i = who;
-        s_m = mine;
-        s_at = at;
-      }
-      items = __shfl_sync(0xffffffffu, mend, 31);
-      before = __shfl_sync(0xffffffffu, nend, 31);
+__global__ void __launch_bounds__(256) paged_attn_join(const __grid_constant__ AttnArgs a) {
+  constexpr int R = kJoinRows, TPR = D / 4, G = 256 / (R * TPR);  // rows; threads per row; groups that share the entries
+  const int c0 = blockIdx.x, r0 = blockIdx.y * R, tid = threadIdx.x;
+  const Shared it = a.shared[c0];
+  const int n = it.pieces * it.copies, nr = min(R, it.rows - r0);
+  if (n == 0 || nr <= 0) return;
+  __shared__ float2 s_ml[kJoin * 8][R];
+  __shared__ float s_red[8][R], s_ref[R], s_sum[R];
+  __shared__ __align__(16) float s_out[G][R][D];
+  const int lc = 31 - __clz(it.copies), apart = it.copies > 1 ? 256 / it.copies : 0;
+  // entry e: copy c of piece k; CTA c0's piece lies in its second slot, those that go on with it use their first
+  auto slot = [&](int e) { return static_cast<int64_t>(e >> lc == 0 ? 2 * c0 + 1 : 2 * (c0 + (e >> lc))); };
+  auto row = [&](int e) {
+    const int c = e & (it.copies - 1);
+    return (c & 1) * 128 + (c >> 1) * apart + r0;
+  };
+  const int r = tid & (R - 1);
+  float top = -INFINITY;
+  if (r < nr)
+    for (int e = tid / R; e < n; e += 256 / R) {
+      const float2 ml = __ldcg(a.part_ml + slot(e) * 256 + row(e) + r);
+      s_ml[e][r] = ml;
+      top = fmaxf(top, ml.x);
     }
-    if (!__any_sync(0xffffffffu, who >= 0) && lane == 0) s_i = -1;
-    if (lane == 0) s_total = before;
-  }
-  __syncthreads();
-  const int i = s_i, m = s_m;
-  if (i < 0) return;
-  const Seq s = seq_of(a.t, a.seq_lens, a.cu, a.n_rows, i);
-  const int rows = min(kRows, s.fresh * a.g - m * kRows);
-  if (r0 >= rows) return;
-  const int64_t total = s_total;
-  const int ctas = static_cast<int>(min(static_cast<int64_t>(grid_ctas), total));
-  const int64_t at = s_at, end = at + item_tiles(s, a.g, a.causal, m);
-  // the CTA that holds list position p is the last whose piece starts at or before it
-  auto owner = [&](int64_t p) { return static_cast<int>(((p + 1) * ctas + total - 1) / total - 1); };
-  const int c0 = owner(at), n = owner(end - 1) - c0 + 1;
-  if (n == 1) return;  // written whole
-  // the pieces' first partial rows, and their weights for the rows of this block
-  __shared__ int64_t s_row[kJoin];
-  __shared__ float s_w[kJoin][32];
-  __shared__ float s_ref[32], s_sum[32];
-  for (int k = tid; k < n; k += 256)
-    s_row[k] = (2 * static_cast<int64_t>(c0 + k) + (at < (c0 + k) * total / ctas ? 0 : 1)) * a.slot_rows + r0;
-  __syncthreads();
-  const int nr = min(32, rows - r0);
-  {  // eight threads per row
-    const int r = tid >> 3, part = tid & 7;
-    float ref = -INFINITY;
-    if (r < nr)
-      for (int k = part; k < n; k += 8) ref = fmaxf(ref, a.part_ml[s_row[k] + r].x);
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, o));
-    const float base = ref == -INFINITY ? 0.0f : ref;
-    float sum = 0.0f;
-    if (r < nr)
-      for (int k = part; k < n; k += 8) {
-        const float2 ml = a.part_ml[s_row[k] + r];
-        const float w = ex2(ml.x - base);
-        s_w[k][r] = w;
-        sum = fmaf(w, ml.y, sum);
-      }
+  for (int o = R; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  if ((tid & 31) < R) s_red[tid >> 5][r] = top;
+  __syncthreads();
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (part == 0 && r < nr) {
-      s_ref[r] = ref;
-      s_sum[r] = sum;
+  for (int w = 0; w < 8; ++w) top = fmaxf(top, s_red[w][r]);
+  const float base = top == -INFINITY ? 0.0f : top;
+  float sum = 0.0f;
+  if (r < nr)
+    for (int e = tid / R; e < n; e += 256 / R) {  // its own entries
+      const float w = ex2(s_ml[e][r].x - base);
+      sum = fmaf(w, s_ml[e][r].y, sum);
+      s_ml[e][r].x = w;
     }
-  }
+#pragma unroll
+  for (int o = R; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   __syncthreads();
-  constexpr int TPR = D / 4, RPB = 256 / TPR;  // threads per row, rows at a time
-  for (int r = tid / TPR; r < nr; r += RPB) {
-    const int x = (tid % TPR) * 4;
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if ((tid & 31) < R) s_red[tid >> 5][r] = sum;
+  __syncthreads();
+  if (tid < R) {
+    float all = 0.0f;
+    for (int w = 0; w < 8; ++w) all += s_red[w][r];
+    s_sum[r] = all;
+    s_ref[r] = top;
+  }
+  const int d = tid / R % TPR, g = tid / (R * TPR);
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (r < nr) {
 #pragma unroll 8
-    for (int k = 0; k < n; ++k) {
-      const float4 v = *reinterpret_cast<const float4*>(a.part_o + (s_row[k] + r) * D + x);
-      const float w = s_w[k][r];
+    for (int e = g; e < n; e += G) {
+      const float4 v = __ldcg(a.part_o + (slot(e) * (D / 4) + d) * 256 + row(e) + r);
+      const float w = s_ml[e][r].x;
       o.x = fmaf(w, v.x, o.x);
       o.y = fmaf(w, v.y, o.y);
       o.z = fmaf(w, v.z, o.z);
       o.w = fmaf(w, v.w, o.w);
     }
-    const float sum = s_sum[r], inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    const int rr = m * kRows + r0 + r, hq = h * a.g + rr % a.g;
-    const int64_t orow = static_cast<int64_t>(s.row0 + rr / a.g) * a.Hq + hq;
-    if (a.out_bf16) {
-      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + orow * D + x) =
-          make_uint2(bf16_pair(o.x * inv, o.y * inv), bf16_pair(o.z * inv, o.w * inv));
-    } else {
-      *reinterpret_cast<float4*>(static_cast<float*>(a.out) + orow * D + x) =
-          make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  }
+  *reinterpret_cast<float4*>(&s_out[g][r][4 * d]) = o;
+  __syncthreads();
+  for (int e = tid; e < nr * TPR; e += 256) {
+    const int q = e / TPR, x = e % TPR * 4;
+    float4 v = *reinterpret_cast<const float4*>(&s_out[0][q][x]);
+#pragma unroll
+    for (int k = 1; k < G; ++k) {
+      const float4 u = *reinterpret_cast<const float4*>(&s_out[k][q][x]);
+      v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
     }
-    if (a.lse && x == 0) a.lse[orow] = sum == 0.0f ? -INFINITY : (s_ref[r] + log2f(sum)) * 0.6931471805599453f;
+    const float all = s_sum[q], inv = all == 0.0f ? 0.0f : 1.0f / all;
+    const int rr = it.m * kRows + r0 + q, tok = rr / a.g;
+    const int64_t orow = static_cast<int64_t>(it.row0 + tok) * a.Hq + it.h * a.g + (rr - tok * a.g);
+    if (a.out_bf16)
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + orow * D + x) =
+          make_uint2(bf16_pair(v.x * inv, v.y * inv), bf16_pair(v.z * inv, v.w * inv));
+    else
+      *reinterpret_cast<float4*>(static_cast<float*>(a.out) + orow * D + x) =
+          make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
+    if (a.lse && x == 0) a.lse[orow] = all == 0.0f ? -INFINITY : (s_ref[q] + log2f(all)) * 0.6931471805599453f;
   }
 }
 
@@ -1168,11 +1167,6 @@ static bool encode_v_map(CUtensorMap* m, const octo_pages* p, int D, int box) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// rows of a partial's slot: no item has more
-static int slot_rows(int64_t n_rows, int g) {
-  return static_cast<int>(std::min<int64_t>(kRows, (n_rows * g + 31) / 32 * 32));
-}
-
 template <int D, int B>
 static cudaError_t launch_attn(const AttnArgs& a, const CUtensorMap& map, int ctas, cudaStream_t st) {
   static LaunchCache cache;
@@ -1181,10 +1175,8 @@ static cudaError_t launch_attn(const AttnArgs& a, const CUtensorMap& map, int ct
   if (e != cudaSuccess) return e;
   paged_attn_kernel<D, B><<<ctas, 512, AttnCfg<D, B>::SMEM, st>>>(a, map);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const int64_t rows = a.n_rows * a.g;
-  const dim3 grid(static_cast<unsigned>(rows / kRows + a.t.n_seqs), a.t.n_heads,
-                  static_cast<unsigned>((std::min<int64_t>(rows, kRows) + 31) / 32));
-  paged_attn_join<D><<<grid, 256, 0, st>>>(a, ctas);
+  const unsigned groups = static_cast<unsigned>((std::min<int64_t>(a.n_rows * a.g, kRows) + kJoinRows - 1) / kJoinRows);
+  paged_attn_join<D><<<dim3(ctas, groups), 256, 0, st>>>(a);
   return cudaGetLastError();
 }
 
@@ -1195,8 +1187,8 @@ extern "C" size_t octo_paged_attn_workspace(const octo_layout* L, int64_t n_rows
   using namespace octo::paged;
   if (check_layout(L) != OCTO_OK || L->d > 128 || n_rows < 0 || n_seqs < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0)
     return 0;
-  const size_t ctas = attn_ctas(), rows = 2 * ctas * slot_rows(n_rows, Hq / Hkv);
-  return 256 + rows * (L->d * sizeof(float) + sizeof(float2)) + ctas * 256 * L->d * sizeof(float);
+  // two partial slots and the row copies of each CTA, whatever the sizes
+  return attn_ctas() * (3 * 256 * L->d * sizeof(float) + 2 * 256 * sizeof(float2) + sizeof(Shared));
 }
 
 extern "C" int octo_paged_attn(const octo_layout* L, const octo_tables* tab, const octo_pages* pages,
@@ -1219,7 +1211,6 @@ extern "C" int octo_paged_attn(const octo_layout* L, const octo_tables* tab, con
   const int g = Hq / pages->n_heads;
   if (g > 256) return OCTO_EUNSUPPORTED;
   if (n_rows * g > INT32_MAX - 1024) return OCTO_EUNSUPPORTED;
-  if (pages->n_heads > 65535) return OCTO_EUNSUPPORTED;  // grid.y limit
   if (n_rows == 0 || table->n_seqs == 0) return OCTO_OK;
   if (!q || !out || !seq_lens || !cu_q) return OCTO_EINVAL;
   if (reinterpret_cast<uintptr_t>(out) % 16 != 0) return OCTO_EINVAL;
@@ -1248,11 +1239,10 @@ extern "C" int octo_paged_attn(const octo_layout* L, const octo_tables* tab, con
   a.out_bf16 = out_dtype == OCTO_BF16;
   a.lse = lse;
   const int ctas = attn_ctas();
-  a.slot_rows = slot_rows(n_rows, g);
-  a.part_ml = reinterpret_cast<float2*>(workspace);
-  const size_t ml = (static_cast<size_t>(2) * ctas * a.slot_rows * sizeof(float2) + 255) / 256 * 256;
-  a.part_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + ml);
-  a.copies = a.part_o + static_cast<size_t>(2) * ctas * a.slot_rows * L->d;
+  a.part_o = static_cast<float4*>(workspace);
+  a.copies = a.part_o + static_cast<size_t>(2) * ctas * (L->d / 4) * 256;
+  a.part_ml = reinterpret_cast<float2*>(a.copies + static_cast<size_t>(ctas) * (L->d / 4) * 256);
+  a.shared = reinterpret_cast<Shared*>(a.part_ml + static_cast<size_t>(2) * ctas * 256);
   const int qe = q_dtype == OCTO_BF16 ? 2 : 4;
   a.q_vec = reinterpret_cast<uintptr_t>(q) % 16 == 0 && q_row_stride * qe % 16 == 0 && q_head_stride * qe % 16 == 0;
   // V comes in boxes that lie inside one page: the largest power of two (8-row swizzle groups) that divides it
