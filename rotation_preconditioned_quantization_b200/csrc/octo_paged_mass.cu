@@ -8,10 +8,14 @@
 // is decoded once however many rows there are.
 //
 // The result is an fp32 statistic, so logits need more than the 11 bits of
-// fp16: keys (times 8) and rotated queries (times scale * log2 e, over a power
-// of two per row) are held as fp16 pairs, hi + lo, and S = K_lo Q_hi + K_hi
-// Q_lo + K_hi Q_hi (the dropped product is below 2^-22). The products are
-// what bounds long chunks: three times the one product's time.
+// fp16, and more than sums on the tensor cores give: those are cut, not
+// rounded, at every step, which biased each weight by 3e-6. So keys and rotated
+// queries (times scale * log2 e, over a power of two per row) are held as fp16
+// pairs whose high parts lie on fixed grids, 2^-12 and 2^-11: the products of
+// high parts and their sums below 2 are whole multiples of 2^-23, exact in
+// fp32 whatever their order, and have accumulators of their own. K_lo Q_hi +
+// K_hi Q_lo, 2^-10 of that, go to a second one (K_lo Q_lo is below 2^-25 per
+// term), and the two are added in fp32. Three products bound long chunks.
 //
 // A first kernel rotates and splits the queries into the tiles the second
 // one's bulk copies bring: 64 rows, hi then lo, already swizzled.
@@ -31,7 +35,7 @@ namespace paged {
 
 constexpr int kQRows = 64;    // rows of a query tile
 constexpr int kUnit = 256;    // slots of a unit
-constexpr float kKeyUp = 8.0f;  // keys are held times 8: their low parts stay clear of fp16's subnormals
+constexpr float kQGrid = 2048.0f, kKGrid = 4096.0f;  // high parts are multiples of 1 / grid
 constexpr int kQPanel = kQRows * 128, kKPanel = 128 * 128;
 
 struct MassArgs {
@@ -53,8 +57,16 @@ struct MassArgs {
   float* mass_out;
   int64_t mass_stride, n_tiles;  // n_tiles: row tiles that the workspace holds per head
   unsigned char* tiles;  // [row tile][head][hi, lo] images
-  float4* rows;          // [row tile][head][64]: 2^e, lse * log2 e, its rounding's factor, slots seen (as int)
+  float* rows;           // [row tile][head][4][64]: 2^e, -lse * log2 e, its rounding's factor, slots seen (as int)
 };
+
+// x as fp16 pair (hi on the grid, lo), low halves of the results
+__device__ __forceinline__ void split2(float x, float y, float grid, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(rintf(x * grid) / grid, rintf(y * grid) / grid);
+  const float2 b = __half22float2(h);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = half2_bits(x - b.x, y - b.y);
+}
 
 __device__ __forceinline__ int query_tiles(const Seq& s, int g) { return (s.fresh * g + kQRows - 1) / kQRows; }
 
@@ -97,7 +109,7 @@ __global__ void __launch_bounds__(256) paged_mass_prep(const __grid_constant__ M
   const int64_t tile = static_cast<int64_t>(blockIdx.x) * a.t.n_heads + h;
   unsigned char* hi = a.tiles + tile * (2 * NP * kQPanel);
   unsigned char* lo = hi + NP * kQPanel;
-  float4* info = a.rows + tile * kQRows;
+  float* info = a.rows + tile * kQRows * 4;
   const float* sg = a.signs + (h % a.table_heads) * D + lane * E;
   // 1 / sqrt(d) of the rotation, the softmax scale and log2 e in one factor
   const float pre = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634 / sqrt(static_cast<double>(D)));
@@ -127,27 +139,29 @@ __global__ void __launch_bounds__(256) paged_mass_prep(const __grid_constant__ M
     unsigned char *ph = hi + sw128(r, lane * E / 8, kQPanel) + (lane * E % 8) * 2, *pl = ph + (lo - hi);
 #pragma unroll
     for (int e = 0; e < E; e += 2) {
-      const float x = v[e] * down, y = v[e + 1] * down;
-      const __half2 t = __floats2half2_rn(x, y);
-      const float2 b = __half22float2(t);
-      *reinterpret_cast<uint32_t*>(ph + 2 * e) = *reinterpret_cast<const uint32_t*>(&t);
-      *reinterpret_cast<uint32_t*>(pl + 2 * e) = half2_bits(x - b.x, y - b.y);
+      uint32_t h, l;
+      split2(v[e] * down, v[e + 1] * down, kQGrid, h, l);
+      *reinterpret_cast<uint32_t*>(ph + 2 * e) = h;
+      *reinterpret_cast<uint32_t*>(pl + 2 * e) = l;
     }
     if (lane == 0) {
-      float4 f = make_float4(0.0f, INFINITY, 0.0f, __int_as_float(0));
+      // a row that is not there, or saw nothing, gives nothing: 2^(x - inf) = 0
+      float up = 0.0f, l2 = -INFINITY, z = 0.0f;
+      int seen = 0;
       if (there) {
         const float l = a.lse[static_cast<int64_t>(s.row0 + tok) * a.Hq + hq];
-        const double l2 = static_cast<double>(l) * 1.4426950408889634;
-        const float up = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23) / kKeyUp;
-        const int seen = a.causal ? max(0, s.len - s.fresh + tok + 1) : s.len;
-        if (l == -INFINITY)  // a row that saw nothing gives nothing
-          f = make_float4(up, INFINITY, 0.0f, __int_as_float(0));
-        else
-          f = make_float4(up, static_cast<float>(l2),
-                          exp2f(static_cast<float>(static_cast<double>(static_cast<float>(l2)) - l2)), __int_as_float(seen));
-        if (!(fabsf(l) < INFINITY) && l != -INFINITY) f.z = 1.0f;  // +inf: weight 0; NaN stays
+        up = __uint_as_float(static_cast<uint32_t>(127 + ex) << 23);
+        if (l != -INFINITY) {
+          const double exact = -static_cast<double>(l) * 1.4426950408889634;
+          l2 = static_cast<float>(exact);
+          z = fabsf(l) < INFINITY ? exp2f(static_cast<float>(exact - static_cast<double>(l2))) : 1.0f;  // (+inf: weight 0; NaN stays)
+          seen = a.causal ? max(0, s.len - s.fresh + tok + 1) : s.len;
+        }
       }
-      info[r] = f;
+      info[r] = up;
+      info[kQRows + r] = l2;
+      info[2 * kQRows + r] = z;
+      info[3 * kQRows + r] = __int_as_float(seen);
     }
   }
 }
@@ -266,61 +280,67 @@ struct MassCfg {
 enum { mKF = 0, mKE = 2, mQF = 4, mQE = 6, mDF = 8, mDE = 12 };  // D barriers: [half][buffer]; the sixteen fill 128 bytes
 
 template <int D, int B>
-__device__ __forceinline__ bool mass_decode(const MassArgs& a, const UnitPlace& place, unsigned char* sm, uint32_t base,
-                                            uint32_t bars, int half) {
+__device__ __forceinline__ bool mass_decode(const MassArgs& a, const UnitPlace& place, unsigned char* sm, uint32_t bars,
+                                            int half) {
   using Cfg = MassCfg<D, B>;
   using K = Code<D, B>;
-  constexpr int W = K::W, T = K::T;
-  const int n = threadIdx.x & 127, lane = threadIdx.x & 31;
-  const uint32_t tab = base + Cfg::TAB + (lane & (Cfg::REP - 1)) * 16;
-  const float* rho = reinterpret_cast<const float*>(sm + Cfg::RHO);
-  uint32_t w[W];
-  auto fetch = [&](const Units& it) {
-    const int slot = it.u * kUnit + half * 128 + n;
-#pragma unroll
-    for (int k = 0; k < W; ++k) w[k] = 0u;
-    if (slot < it.s.len) {
-      const int pg = max(0, page_of(a.t, it.i, slot));
-      const uint32_t* p = a.packed + (static_cast<int64_t>(pg) * a.t.n_heads + it.h) * W * a.t.page_size + page_offset(a.t, slot);
-#pragma unroll
-      for (int k = 0; k < W; ++k) w[k] = __ldg(p + static_cast<int64_t>(k) * a.t.page_size);
-    }
-  };
+  constexpr int W = K::W;
+  const int n = threadIdx.x & 127;
+  const uint32_t copy = (threadIdx.x & (Cfg::REP - 1)) * 16;  // this lane's copy of the table
+  // words are fetched a unit ahead, page ids a unit before that
+  uint32_t w[W], wn[W];
   Units it(a, place);
+  int slot = 0, id = 0;
+  bool held = false, more = false;
+  auto look = [&] {
+    slot = it.u * kUnit + half * 128 + n;
+    held = it.on() && slot < it.s.len;
+    if (held) id = static_cast<int>(load_now(page_entry(a.t, it.i, slot)));
+  };
+  auto fetch = [&] {
+#pragma unroll
+    for (int k = 0; k < W; ++k) wn[k] = 0u;
+    more = it.on();
+    if (!more) return;
+    if (held) {
+      const uint32_t* p = a.packed + (static_cast<int64_t>(max(0, page_checked(a.t, id))) * a.t.n_heads + it.h) * W * a.t.page_size +
+                          page_offset(a.t, slot);
+#pragma unroll
+      for (int k = 0; k < W; ++k) wn[k] = load_now(p + static_cast<int64_t>(k) * a.t.page_size);
+    }
+    do it.next();
+    while (it.on() && it.first >= it.tiles);
+    look();
+  };
   while (it.on() && it.first >= it.tiles) it.next();
-  if (it.on()) fetch(it);
-  for (int c = 0; it.on(); ++c) {
+  look();
+  for (int c = -1; c < 0 || more; ++c) {  // the first turn only fetches
+#pragma unroll
+    for (int k = 0; k < W; ++k) w[k] = wn[k];
+    const bool now = c >= 0;
+    fetch();
+    if (!now) continue;
     if (!bar_wait(bars + 8 * (mKE + half), (c & 1) ^ 1)) return false;
     unsigned char* hi = sm + Cfg::KB + half * 2 * Cfg::KT;
     unsigned char* lo = hi + Cfg::KT;
-#pragma unroll
-    for (int g0 = 0; g0 < T; g0 += 8) {
+    constexpr int GROUPS = (D + 23) / 24;
+#pragma unroll 1
+    for (int grp = 0; grp < GROUPS; ++grp) {
       uint32_t oh[12], ol[12];
 #pragma unroll
       for (int pr = 0; pr < 4; ++pr) {
         uint4 e[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const int i = g0 + 2 * pr + u;
-          e[u] = make_uint4(0u, 0u, 0u, 0u);
-          if (i < T) {
-            if constexpr (Cfg::SPLIT) {
-              const uint32_t code = code_at<K::C, 0>(w, i);
-              float4 d;
-              asm("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                  : "=f"(d.x), "=f"(d.y), "=f"(d.z), "=f"(d.w)
-                  : "r"(tab + ((code & (K::NDIR - 1)) << Cfg::SH)));
-              const float r = rho[code >> K::DIR];
-              const float x = d.x * r, y = d.y * r, z = d.z * r;
-              const __half2 xy = __floats2half2_rn(x, y), zz = __floats2half2_rn(z, 0.0f);
-              const float2 bx = __half22float2(xy), bz = __half22float2(zz);
-              e[u] = make_uint4(*reinterpret_cast<const uint32_t*>(&xy), *reinterpret_cast<const uint32_t*>(&zz),
-                                half2_bits(x - bx.x, y - bx.y), half2_bits(z - bz.x, 0.0f));
-            } else {
-              asm("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                  : "=r"(e[u].x), "=r"(e[u].y), "=r"(e[u].z), "=r"(e[u].w)
-                  : "r"(tab + code_at<K::C, Cfg::SH>(w, i)));
-            }
+          const int i = 2 * pr + u;  // (codes behind the key's last are zeros of the stream, and their halves go nowhere)
+          const uint32_t code = code_at<K::C, Cfg::SPLIT ? 0 : Cfg::SH>(w, i);
+          if constexpr (Cfg::SPLIT) {
+            const float4 d = *reinterpret_cast<const float4*>(sm + Cfg::TAB + ((code & (K::NDIR - 1)) << Cfg::SH));
+            const float r = *reinterpret_cast<const float*>(sm + Cfg::RHO + (code >> K::DIR) * 4);
+            split2(d.x * r, d.y * r, kKGrid, e[u].x, e[u].z);
+            split2(d.z * r, 0.0f, kKGrid, e[u].y, e[u].w);
+          } else {
+            e[u] = *reinterpret_cast<const uint4*>(sm + Cfg::TAB + (code | copy));
           }
         }
         oh[3 * pr] = e[0].x;
@@ -332,19 +352,18 @@ __device__ __forceinline__ bool mass_decode(const MassArgs& a, const UnitPlace& 
       }
 #pragma unroll
       for (int q = 0; q < 3; ++q) {
-        const int chunk = g0 / 8 * 3 + q;
+        const int chunk = grp * 3 + q;
         if (chunk < D / 8) {
           const uint32_t at = sw128(n, chunk, kKPanel);
           *reinterpret_cast<uint4*>(hi + at) = make_uint4(oh[4 * q], oh[4 * q + 1], oh[4 * q + 2], oh[4 * q + 3]);
           *reinterpret_cast<uint4*>(lo + at) = make_uint4(ol[4 * q], ol[4 * q + 1], ol[4 * q + 2], ol[4 * q + 3]);
         }
       }
+      next_codes<K::C>(w);
     }
     fence_async_shared();
     bar_arrive(bars + 8 * (mKF + half));
-    do it.next();
-    while (it.on() && it.first >= it.tiles);
-    if (it.on()) fetch(it);
+    if (!more) break;
   }
   return true;
 }
@@ -363,37 +382,40 @@ __device__ __forceinline__ bool mass_copies(const MassArgs& a, const UnitPlace& 
       const int64_t tile = (it.tile0 + m) * a.t.n_heads + it.h;
       const unsigned char* src = a.tiles + tile * (2 * Cfg::QT);
       if (lane == 0) {
-        bar_expect(bars + 8 * (mQF + st), 2 * Cfg::NP * bytes + n * 16);
+        bar_expect(bars + 8 * (mQF + st), 2 * Cfg::NP * bytes + kQRows * 16);
         issued = c + 1;
         for (int p = 0; p < 2 * Cfg::NP; ++p)
           bulk_in(base + Cfg::QB + st * 2 * Cfg::QT + p * kQPanel, src + p * kQPanel, bytes, bars + 8 * (mQF + st));
-        bulk_in(base + Cfg::ROWS + st * kQRows * 16, a.rows + tile * kQRows, n * 16, bars + 8 * (mQF + st));
+        bulk_in(base + Cfg::ROWS + st * kQRows * 16, a.rows + tile * kQRows * 4, kQRows * 16, bars + 8 * (mQF + st));
       }
       __syncwarp();
     }
   return true;
 }
 
-// S^T of one half (HALF) from the query tile of stage ST, N columns; small
-// products first. Descriptors are constants over the CTA's base.
-template <int D, int B, int HALF, int ST>
-__device__ __forceinline__ void issue_scores(uint32_t base, uint32_t idesc) {
+// S^T of one half from a query tile of N columns: D = K_hi Q_hi, D + 64
+// columns = K_lo Q_hi + K_hi Q_lo. k, q: descriptors of the high parts; the low
+// ones lie KT and QT bytes behind.
+template <int D, int B>
+__device__ __noinline__ void issue_scores(uint32_t d, uint32_t k, uint32_t q, uint32_t idesc) {
   using Cfg = MassCfg<D, B>;
-  constexpr uint32_t d = (HALF * 2 + ST) * kQRows;
+  if (elect_one()) {
+#pragma unroll 1
+    for (int part = 0; part < 3; ++part) {
+      const uint32_t kk = k + (part == 1 ? Cfg::KT >> 4 : 0), qq = q + (part == 2 ? Cfg::QT >> 4 : 0);
+      const uint32_t to = d + (part == 0 ? 0 : kQRows);
 #pragma unroll
-  for (int part = 0; part < 3; ++part) {
-    const uint32_t k = desc_low(base + Cfg::KB + HALF * 2 * Cfg::KT + (part == 0 ? Cfg::KT : 0), 16);
-    const uint32_t q = desc_low(base + Cfg::QB + ST * 2 * Cfg::QT + (part == 1 ? Cfg::QT : 0), 16);
-#pragma unroll
-    for (int s = 0; s < D / 16; ++s) {
-      const uint32_t ko = ((s >> 2) * kKPanel + (s & 3) * 32) >> 4, qo = ((s >> 2) * kQPanel + (s & 3) * 32) >> 4;
-      mma_ss(d, k + ko, q + qo, idesc, part + s > 0);
+      for (int s = 0; s < D / 16; ++s)
+        mma_ss(to, kk + (((s >> 2) * kKPanel + (s & 3) * 32) >> 4), qq + (((s >> 2) * kQPanel + (s & 3) * 32) >> 4), idesc,
+               s > 0 || part == 2);
     }
   }
+  __syncwarp();
 }
 
 template <int D, int B>
 __device__ __forceinline__ bool mass_products(const MassArgs& a, const UnitPlace& place, uint32_t base, uint32_t bars) {
+  using Cfg = MassCfg<D, B>;
   int c = 0, k = 0;
   for (Units it(a, place); it.on(); it.next()) {
     if (it.first >= it.tiles) continue;
@@ -401,16 +423,14 @@ __device__ __forceinline__ bool mass_products(const MassArgs& a, const UnitPlace
       const int st = c & 1;
       if (!bar_wait(bars + 8 * (mQF + st), (c >> 1) & 1)) return false;
       const uint32_t idesc = instr_desc(128, it.cols(m), false, false);
+#pragma unroll 1
       for (int half = 0; half < 2; ++half) {
         if (m == it.first && !bar_wait(bars + 8 * (mKF + half), k & 1)) return false;
         if (!bar_wait(bars + 8 * (mDE + half * 2 + st), ((c >> 1) & 1) ^ 1)) return false;
         tc_after();
+        issue_scores<D, B>((half * 2 + st) * 2 * kQRows, desc_low(base + Cfg::KB + half * 2 * Cfg::KT, 16),
+                           desc_low(base + Cfg::QB + st * 2 * Cfg::QT, 16), idesc);
         if (elect_one()) {
-          if (half) {
-            if (st) issue_scores<D, B, 1, 1>(base, idesc); else issue_scores<D, B, 1, 0>(base, idesc);
-          } else {
-            if (st) issue_scores<D, B, 0, 1>(base, idesc); else issue_scores<D, B, 0, 0>(base, idesc);
-          }
           tc_commit(bars + 8 * (mDF + half * 2 + st));
           if (m + 1 == it.tiles) tc_commit(bars + 8 * (mKE + half));
           if (half == 1) tc_commit(bars + 8 * (mQE + st));
@@ -428,7 +448,7 @@ __device__ __forceinline__ bool mass_sums(const MassArgs& a, const UnitPlace& pl
                                           uint32_t tmem, int half) {
   using Cfg = MassCfg<D, B>;
   const int n = threadIdx.x & 127;
-  const uint32_t D0 = tmem + (static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21) + half * 2 * kQRows;
+  const uint32_t D0 = tmem + (static_cast<uint32_t>((threadIdx.x >> 5) & 3) << 21) + half * 4 * kQRows;
   int c = 0;
   for (Units it(a, place); it.on(); it.next()) {
     const int slot = it.u * kUnit + half * 128 + n, k0 = slot - n;
@@ -448,25 +468,42 @@ __device__ __forceinline__ bool mass_sums(const MassArgs& a, const UnitPlace& pl
       if (!bar_wait(bars + 8 * (mDF + half * 2 + st), (c >> 1) & 1)) return false;
       if (!bar_wait(bars + 8 * (mQF + st), (c >> 1) & 1)) return false;
       tc_after();
-      const float4* rows = reinterpret_cast<const float4*>(sm + Cfg::ROWS) + st * kQRows;
+      const float* rows = reinterpret_cast<const float*>(sm + Cfg::ROWS) + st * kQRows * 4;
       const int cols = it.cols(m);
       // some row of the tile does not see some slot of this half, or the half runs past the sequence
-      const bool masked = __float_as_int(rows[0].w) < k0 + 128;
-      float part[2] = {0.0f, 0.0f};
+      const bool masked = __float_as_int(rows[3 * kQRows]) < k0 + 128;
+      const uint32_t S = D0 + st * 2 * kQRows;
+      float2 part[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+      const float2 gg = make_float2(gamma, gamma);
 #pragma unroll 1
       for (int x0 = 0; x0 < cols; x0 += 16) {
-        uint32_t s[16];
-        tmem_ld16(s, D0 + st * kQRows + x0);
+        uint32_t s[16], t[16];
+        tmem_ld16(s, S + x0);
+        tmem_ld16(t, S + kQRows + x0);
         tc_wait_ld();
 #pragma unroll
-        for (int x = 0; x < 16; ++x) {
-          const float4 r = rows[x0 + x];
-          float w = ex2(fmaf(__uint_as_float(s[x]), gamma * r.x, -r.y));
-          if (masked && slot >= __float_as_int(r.w)) w = 0.0f;
-          part[x & 1] = fmaf(w, r.z, part[x & 1]);
+        for (int x = 0; x < 16; x += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(rows + x0 + x);
+          const float4 l = *reinterpret_cast<const float4*>(rows + kQRows + x0 + x);
+          const float4 z = *reinterpret_cast<const float4*>(rows + 2 * kQRows + x0 + x);
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            const int i = x + 2 * y;
+            const float2 sc = add_f32x2(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])),
+                                        make_float2(__uint_as_float(t[i]), __uint_as_float(t[i + 1])));
+            const float2 e = fma_f32x2(sc, mul_f32x2(gg, y ? make_float2(f.z, f.w) : make_float2(f.x, f.y)),
+                                       y ? make_float2(l.z, l.w) : make_float2(l.x, l.y));
+            float2 w = make_float2(ex2(e.x), ex2(e.y));
+            if (masked) {
+              if (slot >= __float_as_int(rows[3 * kQRows + x0 + i])) w.x = 0.0f;
+              if (slot >= __float_as_int(rows[3 * kQRows + x0 + i + 1])) w.y = 0.0f;
+            }
+            part[y] = fma_f32x2(w, y ? make_float2(z.z, z.w) : make_float2(z.x, z.y), part[y]);
+          }
         }
       }
-      sum += part[0] + part[1];
+      part[0] = add_f32x2(part[0], part[1]);
+      sum += part[0].x + part[0].y;
       tc_before();
       bar_arrive(bars + 8 * (mDE + half * 2 + st));
       bar_arrive(bars + 8 * (mQE + st));
@@ -488,7 +525,7 @@ __global__ void __launch_bounds__(576, 1) paged_mass_kernel(const __grid_constan
   float* s_dir = reinterpret_cast<float*>(sm + Cfg::DIR);
   float* s_rho = reinterpret_cast<float*>(sm + Cfg::RHO);
   if (tid < (1 << (B + 1))) s_dir[tid] = a.dir_c[tid];
-  if (tid < K::NRHO) s_rho[tid] = a.rho_c[tid] * kKeyUp;
+  if (tid < K::NRHO) s_rho[tid] = a.rho_c[tid];
   if (warp == 17) {
     const UnitPlace p = find_units(a, lane);
     if (lane == 0) s_place = p;
@@ -516,11 +553,9 @@ __global__ void __launch_bounds__(576, 1) paged_mass_kernel(const __grid_constan
       if constexpr (Cfg::SPLIT) {
         v = make_uint4(__float_as_uint(d.x), __float_as_uint(d.y), __float_as_uint(d.z), 0u);
       } else {
-        const float r = s_rho[e >> K::DIR], x = d.x * r, y = d.y * r, z = d.z * r;
-        const __half2 xy = __floats2half2_rn(x, y), zz = __floats2half2_rn(z, 0.0f);
-        const float2 bx = __half22float2(xy), bz = __half22float2(zz);
-        v = make_uint4(*reinterpret_cast<const uint32_t*>(&xy), *reinterpret_cast<const uint32_t*>(&zz),
-                       half2_bits(x - bx.x, y - bx.y), half2_bits(z - bz.x, 0.0f));
+        const float r = s_rho[e >> K::DIR];
+        split2(d.x * r, d.y * r, kKGrid, v.x, v.z);
+        split2(d.z * r, 0.0f, kKGrid, v.y, v.w);
       }
 #pragma unroll
       for (int k = 0; k < Cfg::REP; ++k) *reinterpret_cast<uint4*>(sm + Cfg::TAB + (e << Cfg::SH) + k * 16) = v;
@@ -535,7 +570,7 @@ __global__ void __launch_bounds__(576, 1) paged_mass_kernel(const __grid_constan
     if (warp < 8) {
       ok = mass_sums<D, B>(a, place, sm, bars, tmem, warp >> 2);
     } else if (warp < 16) {
-      ok = mass_decode<D, B>(a, place, sm, base, bars, (warp - 8) >> 2);
+      ok = mass_decode<D, B>(a, place, sm, bars, (warp - 8) >> 2);
     } else if (warp == 16) {
       ok = mass_products<D, B>(a, place, base, bars);
       if (!ok) {  // products in flight end before tensor memory is given back (a fresh barrier in the table's place)
@@ -652,7 +687,7 @@ extern "C" int octo_paged_mass(const octo_layout* L, const octo_tables* tab, con
   a.n_tiles = most_tiles(n_rows, table->n_seqs, g);
   const size_t tiles = static_cast<size_t>(a.n_tiles) * pages->n_heads;
   a.tiles = static_cast<unsigned char*>(workspace);
-  a.rows = reinterpret_cast<float4*>(a.tiles + tiles * (static_cast<size_t>(2) * kQRows * L->d * 2));
+  a.rows = reinterpret_cast<float*>(a.tiles + tiles * (static_cast<size_t>(2) * kQRows * L->d * 2));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (L->d == 64)

@@ -9,11 +9,13 @@ Error bounds that the tests use, u = eps / 2 of a type (bf16 2^-8, fp16 2^-11, f
   accumulation, 4 d * 2^-24 of the sum of magnitudes. Weights are then off by a factor in exp(+-2 Dmax) (numerator and
   denominator), and by u(bf16) = 2^-8 from rounding the weight: |out - ref| <= (expm1(2 Dmax) + 2^-8 + 2^-16) * sum p |v|
   + u(out) |ref|; |lse - ref| <= Dmax + 2^-20 (1 + |ref|).
-* a logit of ``paged_mass`` comes from hi + lo pairs: the dropped product and the two lo roundings are below 2^-22 each,
-  query entries below 2^-25 of their row's largest fall to fp16's subnormals, the fp32 accumulation of 3 d terms rounds
-  by at most 3 d * 2^-24 of the sum of magnitudes, and the tensor core truncates (twice the rounding): D' = |scale| *
-  gamma * (sum |q~| |u| * (3 * 2^-22 + 6 d * 2^-24) + 2^-25 sqrt(d) max|q~|) + 2^-22 (|logit| + |lse|). A mass is off by
-  at most sum w * (expm1(D') + 2^-21 + rows * 2^-24) + 2^-23 * |mass|.
+* a logit of ``paged_mass`` comes from hi + lo pairs, high parts on grids of 2^-11 (queries, scaled so that their row's
+  largest is below 1 and at least 1/2: units of it cost a factor 2) and 2^-12 (keys): the dropped product is at most
+  2^-12 * 2^-13 per term, d terms; the low parts round by 2^-23 and 2^-24, against sum |u| <= sqrt(d) and |q~|; the fp32
+  accumulation of 2 d small terms and the sums round by less than 6 d * 2^-24 of the sum of magnitudes (the tensor core
+  truncates: twice the rounding). D' = |scale| * gamma * (sum |q~| |u| * (3 * 2^-22 + 6 d * 2^-24) + (2^-24 d + 2^-22
+  sqrt(d)) max|q~|) + 2^-22 (|logit| + |lse|). A mass is off by at most sum w * (expm1(D') + 2^-21 + rows * 2^-24) +
+  2^-23 * |mass|.
 """
 
 from __future__ import annotations
@@ -158,7 +160,7 @@ def mass(pool, q, lse, cu, prev, decay, causal=True, scale=None):
                 ls = np.where(np.isfinite(ls), ls, 0)
                 x = np.where(ok, np.exp(np.where(ok, L - ls, 0)), 0)
                 D = abs(scale) * gm * (np.abs(qr) @ np.abs(u).T * (3 * 2.0 ** -22 + 6 * d * 2.0 ** -24) +
-                                       2.0 ** -25 * np.sqrt(d) * np.abs(qr).max(-1, keepdims=True))
+                                       (2.0 ** -24 * d + 2.0 ** -22 * np.sqrt(d)) * np.abs(qr).max(-1, keepdims=True))
                 D = D + 2.0 ** -22 * (np.abs(L) + np.abs(ls))
                 w = x.sum(0)
                 tw = (x * (np.expm1(D) + 2.0 ** -21 + len(x) * 2.0 ** -24)).sum(0)
