@@ -263,13 +263,15 @@ struct MassCfg {
   static constexpr int NP = D / 64;
   static constexpr int KT = NP * kKPanel;          // one part (hi or lo) of a 128-slot key tile
   static constexpr int QT = NP * kQPanel;          // one part of a query tile
-  // b <= 3: every signed code as {x, y hi | z hi | x, y lo | z lo} (fp16
-  // pairs), 16 bytes; b = 4: the unit directions in fp32, times the norm
-  // level in registers (8192 codes would need 128 KB).
-  static constexpr bool SPLIT = B == 4;
-  static constexpr int NE = SPLIT ? K::NDIR : 1 << K::C;
-  static constexpr int REP = NE <= 128 ? 8 : 1;
-  static constexpr int SH = 4 + (REP == 8 ? 3 : 0);
+  // Entries of 16 bytes, 8 copies of each: the lanes of a quarter-warp read
+  // distinct banks (one copy of every signed code at b = 3 met 2.5 a bank, and
+  // the lookups bound single tokens). b = 2 every signed code, b = 3 those of
+  // the positive quadrant, as {x, y hi | z hi | x, y lo | z lo} (fp16 pairs);
+  // b = 4 the quadrant's unit directions in fp32, times the norm level in
+  // registers. A code's signs flip sign bits (the codebook and the inverse map
+  // are odd in x and in y).
+  static constexpr bool SPLIT = B == 4, QUAD = B > 2;
+  static constexpr int NE = B == 2 ? 128 : 256, REP = 8, SH = 4 + 3;
   static constexpr int KB = 0, QB = 4 * KT, TAB = QB + 4 * QT, RHO = TAB + (NE << SH), ROWS = RHO + 32;
   static constexpr int BARS = ROWS + 2 * kQRows * 16, PLACE = BARS + 16 * 8, TMEM = PLACE + 40, DIR = PLACE + 48,
                        SMEM = DIR + 128;
@@ -333,14 +335,23 @@ __device__ __forceinline__ bool mass_decode(const MassArgs& a, const UnitPlace& 
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           const int i = 2 * pr + u;  // (codes behind the key's last are zeros of the stream, and their halves go nowhere)
-          const uint32_t code = code_at<K::C, Cfg::SPLIT ? 0 : Cfg::SH>(w, i);
+          const uint32_t code = code_at<K::C, Cfg::SH>(w, i);
+          constexpr int sx = 2 * B + Cfg::SH, sy = sx + 1;  // sign bits in code
+          uint32_t at = code;
+          if constexpr (Cfg::QUAD) at = code & ((1u << sx) - (1u << Cfg::SH));
+          if constexpr (B == 3) at |= (code >> 2) & (3u << sx);  // the norm level's two bits behind
+          e[u] = *reinterpret_cast<const uint4*>(sm + Cfg::TAB + (at | copy));
           if constexpr (Cfg::SPLIT) {
-            const float4 d = *reinterpret_cast<const float4*>(sm + Cfg::TAB + ((code & (K::NDIR - 1)) << Cfg::SH));
-            const float r = *reinterpret_cast<const float*>(sm + Cfg::RHO + (code >> K::DIR) * 4);
-            split2(d.x * r, d.y * r, kKGrid, e[u].x, e[u].z);
-            split2(d.z * r, 0.0f, kKGrid, e[u].y, e[u].w);
-          } else {
-            e[u] = *reinterpret_cast<const uint4*>(sm + Cfg::TAB + (code | copy));
+            const float r = *reinterpret_cast<const float*>(sm + Cfg::RHO + (code >> (K::DIR + Cfg::SH)) * 4);
+            const float x = __uint_as_float(e[u].x ^ ((code << (31 - sx)) & 0x80000000u)) * r;
+            const float y = __uint_as_float(e[u].y ^ ((code << (31 - sy)) & 0x80000000u)) * r;
+            const float z = __uint_as_float(e[u].z) * r;
+            split2(x, y, kKGrid, e[u].x, e[u].z);
+            split2(z, 0.0f, kKGrid, e[u].y, e[u].w);
+          } else if constexpr (Cfg::QUAD) {  // s_xi to bit 15, s_eta to bit 31
+            const uint32_t flip = ((code << (15 - sx)) & 0x8000u) | ((code << (31 - sy)) & 0x80000000u);
+            e[u].x ^= flip;
+            e[u].z ^= flip;
           }
         }
         oh[3 * pr] = e[0].x;
@@ -475,12 +486,7 @@ __device__ __forceinline__ bool mass_sums(const MassArgs& a, const UnitPlace& pl
       const uint32_t S = D0 + st * 2 * kQRows;
       float2 part[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
       const float2 gg = make_float2(gamma, gamma);
-#pragma unroll 1
-      for (int x0 = 0; x0 < cols; x0 += 16) {
-        uint32_t s[16], t[16];
-        tmem_ld16(s, S + x0);
-        tmem_ld16(t, S + kQRows + x0);
-        tc_wait_ld();
+      auto weigh = [&](const uint32_t (&s)[16], const uint32_t (&t)[16], int x0) {
 #pragma unroll
         for (int x = 0; x < 16; x += 4) {
           const float4 f = *reinterpret_cast<const float4*>(rows + x0 + x);
@@ -501,6 +507,14 @@ __device__ __forceinline__ bool mass_sums(const MassArgs& a, const UnitPlace& pl
             part[y] = fma_f32x2(w, y ? make_float2(z.z, z.w) : make_float2(z.x, z.y), part[y]);
           }
         }
+      };
+#pragma unroll 1
+      for (int x0 = 0; x0 < cols; x0 += 16) {
+        uint32_t s[16], t[16];
+        tmem_ld16(s, S + x0);
+        tmem_ld16(t, S + kQRows + x0);
+        tc_wait_ld();
+        weigh(s, t, x0);
       }
       part[0] = add_f32x2(part[0], part[1]);
       sum += part[0].x + part[0].y;
@@ -548,12 +562,12 @@ __global__ void __launch_bounds__(576, 1) paged_mass_kernel(const __grid_constan
   const UnitPlace place = s_place;
   if (place.count > 0) {
     for (int e = tid; e < Cfg::NE; e += Cfg::THREADS) {
-      const float3 d = field_direction<B>(e & (K::NDIR - 1), s_dir);
+      const float3 d = field_direction<B>(Cfg::QUAD ? e & ((1 << 2 * B) - 1) : e & (K::NDIR - 1), s_dir);
       uint4 v;
       if constexpr (Cfg::SPLIT) {
         v = make_uint4(__float_as_uint(d.x), __float_as_uint(d.y), __float_as_uint(d.z), 0u);
       } else {
-        const float r = s_rho[e >> K::DIR];
+        const float r = s_rho[Cfg::QUAD ? e >> (2 * B) : e >> K::DIR];
         split2(d.x * r, d.y * r, kKGrid, v.x, v.z);
         split2(d.z * r, 0.0f, kKGrid, v.y, v.w);
       }
