@@ -312,8 +312,9 @@ def _chunk(layout, tables, q, cache, page_table, seq_lens, cu_q):
             raise ValueError(f"{rows} query rows over {B} sequences: cu_q is needed")
         cu_q = torch.arange(B + 1, dtype=_I32, device=q.device) * (rows // B)
     _vector(cu_q, "cu_q", B + 1)
+    t = _table(page_table, B)
     _same_device(cache.index, q, page_table, seq_lens, cu_q, tables.dir_c, tables.signs)
-    return dt, rows, Hq, B, cu_q, _table(page_table, B)
+    return dt, rows, Hq, B, cu_q, t
 
 
 def paged_attn_workspace_bytes(layout: api.Layout, rows: int, B: int, Hq: int, Hkv: int) -> int:

@@ -187,6 +187,12 @@ def test_evict_long(cuda_ok):
     _evict(3, 64, 2, 256, 1, [100001], 30011, 4, 1000)
 
 
+@pytest.mark.parametrize("slots", [4096, 4097, 139904, 139905])
+def test_evict_at_the_bounds_of_its_variants(cuda_ok, slots):
+    """One block or four per head, ordered bits held in shared memory or read again: the choice goes by the table's slots."""
+    _evict(slots, 64, 2, 256, 1, [slots - 1, 300], 257, 3, 50, slots=slots, values=False)
+
+
 def test_evict_into_another_pool_and_keys_only(cuda_ok):
     _evict(4, 128, 3, 64, 2, [500, 10], 200, 2, 30, other=True)
     _evict(5, 128, 3, 64, 2, [500, 10], 200, 2, 30, values=False)
