@@ -171,7 +171,24 @@ __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
-__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Loads from tensor memory are complete, those into r among them. The values
+// are made new behind the wait: nothing else keeps the compiler from using
+// the registers before it.
+template <int N>
+__device__ __forceinline__ void landed(uint32_t (&r)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+template <int N>
+__device__ __forceinline__ void tc_wait_ld(uint32_t (&r)[N]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+  landed(r);
+}
+template <int N>
+__device__ __forceinline__ void tc_wait_ld(uint32_t (&r)[N], uint32_t (&q)[N]) {
+  tc_wait_ld(r);
+  landed(q);
+}
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Shared-memory matrix descriptors with the 128-byte swizzle, as two words:

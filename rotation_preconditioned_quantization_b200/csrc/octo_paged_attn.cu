@@ -18,7 +18,8 @@
 // Warps (16): 0-3 and 4-7 the softmax of query tile 0 and 1 (a thread owns a
 // row: no shuffles), and before it the rotation of their queries; 8-11 decode
 // key tiles, a thread per slot, one ahead of the products; 12 issues the
-// products; 13 copies V.
+// products; 13 copies V and zeroes
+// the rows behind a sequence's end.
 //
 // Items of at most 128 rows would leave the second query tile empty and the
 // softmax of few rows to few warps. There both S and O pairs serve the one
@@ -354,19 +355,6 @@ __device__ __forceinline__ bool decode_role(const AttnArgs& a, const Place& plac
       }
       fence_async_shared();
       bar_arrive(bars + 8 * (kKF + st));
-      // V rows behind the sequence's end hold whatever the page held: zero
-      // them once the copy is in (0 * NaN would reach the output)
-      if (valid < kKeys) {
-        if (!bar_wait(bars + 8 * (kVF + st), (c >> 1) & 1)) return false;
-        unsigned char* vt = sm + Cfg::V + st * Cfg::TILE;
-        if (n >= valid) {
-#pragma unroll
-          for (int q = 0; q < D / 8; ++q)
-            *reinterpret_cast<uint4*>(vt + (q >> 3) * kPanel + n * 128 + (q & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-        }
-        fence_async_shared();
-        bar_arrive(bars + 8 * (kVZ + st));
-      }
     }
   }
   return true;
@@ -374,8 +362,8 @@ __device__ __forceinline__ bool decode_role(const AttnArgs& a, const Place& plac
 
 // ---- V copies ---------------------------------------------------------------
 template <int D, int B>
-__device__ __forceinline__ bool v_role(const AttnArgs& a, const Place& place, const CUtensorMap* map, uint32_t base,
-                                       uint32_t bars, int& issued) {
+__device__ __forceinline__ bool v_role(const AttnArgs& a, const Place& place, const CUtensorMap* map, unsigned char* sm,
+                                       uint32_t base, uint32_t bars, int& issued) {
   using Cfg = AttnCfg<D, B>;
   const int lane = threadIdx.x & 31;
   int c = 0;
@@ -399,6 +387,21 @@ __device__ __forceinline__ bool v_role(const AttnArgs& a, const Place& place, co
                  pg * a.t.n_heads + it.h, bars + 8 * (kVF + st));
       }
       __syncwarp();
+      // V rows behind the sequence's end hold whatever the page or the stage
+      // held: zero them once the copy is in (0 * NaN would reach the output).
+      // This warp alone can: it knows that the stage's last products are done
+      // and that the copy it waits for is the stage's newest.
+      if (valid < kKeys) {
+        if (!bar_wait(bars + 8 * (kVF + st), (c >> 1) & 1)) return false;
+        unsigned char* vt = sm + Cfg::V + st * Cfg::TILE;
+        for (int n = valid * 8 + lane; n < kKeys * 8; n += 32) {
+#pragma unroll
+          for (int p = 0; p < Cfg::NP; ++p)
+            *reinterpret_cast<uint4*>(vt + p * kPanel + n * 16) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_async_shared();
+        bar_arrive(bars + 8 * (kVZ + st));
+      }
     }
   }
   return true;
@@ -659,7 +662,7 @@ struct Row {
       for (int d = 0; d < D; d += 16) {
         uint32_t o[16];
         tmem_ld16(o, O + d);
-        tc_wait_ld();
+        tc_wait_ld(o);
 #pragma unroll
         for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * keep);
         tmem_st16(O + d, o);
@@ -681,7 +684,7 @@ struct Row {
 #pragma unroll 1
     for (int c = col0; c < col0 + cols; c += 32) {
       tmem_ld32(s, S + c);
-      tc_wait_ld();
+      tc_wait_ld(s);
       logits_any(y, s, gm + c, left - c, 0.0f);
       top = largest(y, top);
     }
@@ -692,7 +695,7 @@ struct Row {
     for (int c = col0; c < col0 + cols; c += 32) {
       if (cols > 32) {
         tmem_ld32(s, S + c);
-        tc_wait_ld();
+        tc_wait_ld(s);
         logits_any(y, s, gm + c, left - c, 0.0f);
       }
 #pragma unroll
@@ -713,7 +716,7 @@ struct Row {
     for (int c = 0; c < kKeys; c += 64) {
       tmem_ld32(s, S + c);
       tmem_ld32(t, S + c + 32);
-      tc_wait_ld();
+      tc_wait_ld(s, t);
 #pragma unroll
       for (int x = 0; x < 32; x += 2) {
         top[0] = max3_abs(top[0], __uint_as_float(s[x]), __uint_as_float(s[x + 1]));
@@ -727,7 +730,7 @@ struct Row {
 #pragma unroll 1
       for (int c = 0; c < kKeys; c += 32) {
         tmem_ld32(s, S + c);
-        tc_wait_ld();
+        tc_wait_ld(s);
         logits(y, s, gm + c, 0.0f);
         high = largest(y, high);
       }
@@ -740,7 +743,7 @@ struct Row {
       float2 y[16];
       tmem_ld32(s, S + c);
       tmem_ld32(t, S + c + 32);
-      tc_wait_ld();
+      tc_wait_ld(s, t);
       logits(y, s, gm + c, shift);
       weights(y, S + c / 2, u);
       logits(y, t, gm + c + 32, shift);
@@ -868,7 +871,7 @@ __device__ __forceinline__ bool softmax_role(const AttnArgs& a, const Place& pla
         for (int k = 0; k < D; k += 16) {
           uint32_t o[16];
           tmem_ld16(o, row.O + k);
-          tc_wait_ld();
+          tc_wait_ld(o);
           if (there) {
 #pragma unroll
             for (int y = 0; y < 4; ++y)  // (a row without a slot here may find anything in O)
@@ -889,7 +892,7 @@ __device__ __forceinline__ bool softmax_role(const AttnArgs& a, const Place& pla
           float v[32];
           if (nt > 0) {
             tmem_ld32(o, row.O + k);
-            tc_wait_ld();
+            tc_wait_ld(o);
           }
           // a row that saw nothing gives 0
 #pragma unroll
@@ -919,7 +922,7 @@ __device__ __forceinline__ bool softmax_role(const AttnArgs& a, const Place& pla
         for (int k = 0; k < D; k += 16) {
           uint32_t o[16];
           tmem_ld16(o, row.O + k);
-          tc_wait_ld();
+          tc_wait_ld(o);
           if (there) {
 #pragma unroll
             for (int y = 0; y < 4; ++y)  // a copy without a slot may hold anything
@@ -985,7 +988,7 @@ __global__ void __launch_bounds__(512, 1) paged_attn_kernel(const __grid_constan
       bar_init(bars + 8 * (kKE + q), 1);
       bar_init(bars + 8 * (kVF + q), 1);
       bar_init(bars + 8 * (kVE + q), 1);
-      bar_init(bars + 8 * (kVZ + q), 128);
+      bar_init(bars + 8 * (kVZ + q), 32);
     }
     bar_init(bars + 8 * kEND, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -1027,13 +1030,13 @@ __global__ void __launch_bounds__(512, 1) paged_attn_kernel(const __grid_constan
         ok = mma_role<D, B>(a, place, base, bars);
         // products in flight end before tensor memory is given back
         if (!ok) {
-          if (lane == 0) tc_commit(bars + 8 * kEND);
+          if (elect_one()) tc_commit(bars + 8 * kEND);
           __syncwarp();
           bar_wait(bars + 8 * kEND, 0);
         }
       } else if (warp == 13) {
         int issued = 0;
-        ok = v_role<D, B>(a, place, &vmap, base, bars, issued);
+        ok = v_role<D, B>(a, place, &vmap, sm, base, bars, issued);
         // copies in flight end before the CTA does
         for (int c = max(0, issued - 2); c < issued; ++c) bar_wait(bars + 8 * (kVF + (c & 1)), (c >> 1) & 1);
       }

@@ -513,7 +513,7 @@ __device__ __forceinline__ bool mass_sums(const MassArgs& a, const UnitPlace& pl
         uint32_t s[16], t[16];
         tmem_ld16(s, S + x0);
         tmem_ld16(t, S + kQRows + x0);
-        tc_wait_ld();
+        tc_wait_ld(s, t);
         weigh(s, t, x0);
       }
       part[0] = add_f32x2(part[0], part[1]);
