@@ -709,7 +709,9 @@ struct Row {
   // all 1. First the largest |product|: times the tile's largest norm it
   // bounds the logits, and hardly ever asks for a look at the logits
   // themselves.
-  __device__ __forceinline__ void weigh_full(const float* gm, float gmax, bool o_set) {
+  // (`there`: the lane holds a row. The others' S is left over from any item;
+  // neither they nor other rows have a say in what a row does.)
+  __device__ __forceinline__ void weigh_full(const float* gm, float gmax, bool there, bool o_set) {
     uint32_t s[32], t[32];
     float top[2] = {0.0f, 0.0f};
 #pragma unroll 1
@@ -724,7 +726,8 @@ struct Row {
       }
     }
     // (a NaN among them, or an infinite norm, fails the comparison)
-    if (!__all_sync(0xffffffffu, fmaxf(top[0], top[1]) * gmax <= ref + 100.0f)) {
+    const bool ask = there && !(fmaxf(top[0], top[1]) * gmax <= ref + 100.0f);
+    if (__any_sync(0xffffffffu, ask)) {
       float high = -INFINITY;
       float2 y[16];
 #pragma unroll 1
@@ -734,7 +737,7 @@ struct Row {
         logits(y, s, gm + c, 0.0f);
         high = largest(y, high);
       }
-      follow(high, o_set);
+      follow(ask ? high : -INFINITY, o_set);
     }
     const float shift = ref == -INFINITY ? 0.0f : -ref;
     float2 u = make_float2(0.0f, 0.0f), v = make_float2(0.0f, 0.0f);
@@ -825,7 +828,7 @@ __device__ __forceinline__ bool softmax_role(const AttnArgs& a, const Place& pla
           const bool o_set = two ? j > 0 : j > 1;
           if (cols == kKeys && plain && !masked) {
             const float4 g4 = *reinterpret_cast<const float4*>(sm + Cfg::GMAX + ((c + j) % Cfg::GS) * 16);
-            row.weigh_full(gm, max3(g4.x, g4.y, fmaxf(g4.z, g4.w)), o_set);
+            row.weigh_full(gm, max3(g4.x, g4.y, fmaxf(g4.z, g4.w)), there, o_set);
           } else {
             row.weigh_any(gm, col0, cols, left, o_set);
           }
