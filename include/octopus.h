@@ -406,14 +406,15 @@ OCTO_API int octo_paged_write(const octo_layout* L, const octo_pages* pages, con
  *   q    device, row r head h at q + r*q_row_stride + h*q_head_stride
  *        (elements), q_dtype OCTO_F32 or OCTO_BF16, d contiguous.
  *        Query head hq reads KV head hq / (Hq / n_heads).
- *   out  device [n_rows][Hq][d], out_dtype OCTO_F32 or OCTO_BF16, 16-byte aligned.
+ *   out  device [n_rows][Hq][d], out_dtype OCTO_F32 or OCTO_BF16, 16-byte aligned; must not overlap q.
  *   lse  device fp32 [n_rows][Hq] ln sum exp(logits), or NULL.
  *   workspace  device, 256-byte aligned, octo_paged_attn_workspace() bytes of
  *        scratch; nothing in it needs to be kept or cleared between calls.
  *        Calls that share it must not overlap on the GPU.
  * Keys and queries enter the tensor cores as fp16 (queries scaled by a power
  * of two per row), weights and V as bf16; sums and softmax statistics are
- * fp32. Values of slots that a row does not see, but another row of its
+ * fp32 (out is divided by the sum of the rounded weights, lse is that of the
+ * unrounded ones). Values of slots that a row does not see, but another row of its
  * sequence does, must be finite. Two launches.
  * Supported: d in {64, 128}, b in {2, 3, 4}, Hq / n_heads <= 256.
  * Errors: OCTO_EINVAL, OCTO_EUNSUPPORTED, OCTO_EWORKSPACE. n_rows == 0
@@ -435,7 +436,8 @@ OCTO_API int octo_paged_attn(const octo_layout* L, const octo_tables* tables, co
  *   mass_in, mass_out device fp32 [n_seqs][n_heads][mass_stride] (the same
  *        array, or not overlapping); mass_in NULL reads as 0. Slots at and
  *        beyond mass_stride are not counted (OCTO_PAGED_BAD_LENGTH).
- * Logits are formed from fp16 pairs (hi + lo, 22 bits) on the tensor cores.
+ * Logits are formed from fp16 pairs (hi + lo) on the tensor cores, the high
+ * parts on fixed grids whose products sum exactly: about fp32's precision.
  * Two launches. Supported shapes, workspace rules and errors as
  * octo_paged_attn. */
 OCTO_API size_t octo_paged_mass_workspace(const octo_layout* L, int64_t n_rows, int n_seqs, int Hq, int Hkv);

@@ -78,6 +78,7 @@ struct AttnArgs {
   float4* part_o;  // [slots][D / 4][256]: lanes own rows, so their accesses are contiguous
   float4* copies;  // [CTAs][D / 4][256]: the row copies of an item of at most 128 rows, on their way to their sum
   float2* part_ml; // [slots][256]
+  float* part_e;   // [slots][256]: sums of the weights before their rounding, where lse is asked for
   Shared* shared;  // [CTAs]
 };
 
@@ -607,10 +608,10 @@ __device__ __forceinline__ float max3_abs(float a, float b, float c) {
 // O. Weights are 2^(logit - ref) for a reference that needs only be near
 // (bf16 and fp32 keep their precision whatever the exponent): it is set by a
 // row's first slots and raised when a logit might pass it by 100.
-template <int D>
+template <int D, bool LSE>  // LSE: lse is asked for
 struct Row {
   uint32_t S, O;
-  float ref, sum, up;  // up: 2^ex of the row's queries
+  float ref, sum, exact, up;  // exact: the sum before rounding, for lse alone; up: 2^ex of the row's queries
 
   // Logits less the reference of 32 slots from their raw products: times the norms g.
   __device__ __forceinline__ void logits(float2 (&y)[16], const uint32_t (&s)[32], const float* gm, float shift) const {
@@ -637,16 +638,28 @@ struct Row {
     }
   }
 
-  // bf16 weights of 32 slots to column c of P; their sum
-  __device__ __forceinline__ void weights(const float2 (&y)[16], uint32_t c, float2& total) const {
+  // Weights of 32 slots to column c of P, rounded to bf16 (V's type, which the
+  // product shares), and their sum. Summed as rounded, so that output rows
+  // are averages with the very weights used, and one slot that outweighs the
+  // rest costs nothing: error against 64 bits on 512 tokens over 32768 slots
+  // 1.84e-3 (1.6e-3 of it the output's rounding), 2.4e-3 with the sum of the
+  // unrounded weights, which took 342 us instead of 368. lse, an fp32 value,
+  // is formed from the latter.
+  __device__ __forceinline__ void weights(const float2 (&y)[16], uint32_t c, float2& total, float2& before) const {
     uint32_t p[16];
 #pragma unroll
     for (int x = 0; x < 16; ++x) {
       const float2 e = make_float2(ex2(y[x].x), ex2(y[x].y));
-      total = add_f32x2(total, e);
       p[x] = bf16_pair(e.x, e.y);
+      if constexpr (LSE) before = add_f32x2(before, e);
     }
     tmem_st16(c, p);
+#pragma unroll
+    for (int x = 0; x < 16; x += 4) {  // (as a tree: a chain of sums would wait for each)
+      const float2 a = add_f32x2(make_float2(bf16_lo(p[x]), bf16_hi(p[x])), make_float2(bf16_lo(p[x + 1]), bf16_hi(p[x + 1])));
+      const float2 b = add_f32x2(make_float2(bf16_lo(p[x + 2]), bf16_hi(p[x + 2])), make_float2(bf16_lo(p[x + 3]), bf16_hi(p[x + 3])));
+      total = add_f32x2(total, add_f32x2(a, b));
+    }
   }
 
   // A row's reference follows its largest logit of the tile where that passes
@@ -657,6 +670,7 @@ struct Row {
     const float keep = raise ? ex2(ref - top) : 1.0f;
     if (raise) ref = top;
     sum *= keep;
+    if constexpr (LSE) exact *= keep;
     if (o_set) {
 #pragma unroll 1
       for (int d = 0; d < D; d += 16) {
@@ -690,7 +704,7 @@ struct Row {
     }
     follow(top, o_set);
     const float shift = ref == -INFINITY ? 0.0f : -ref;
-    float2 total = make_float2(0.0f, 0.0f);
+    float2 total = make_float2(0.0f, 0.0f), before = total;
 #pragma unroll 1
     for (int c = col0; c < col0 + cols; c += 32) {
       if (cols > 32) {
@@ -700,9 +714,10 @@ struct Row {
       }
 #pragma unroll
       for (int x = 0; x < 16; ++x) y[x] = add_f32x2(y[x], make_float2(shift, shift));
-      weights(y, S + c / 2, total);
+      weights(y, S + c / 2, total, before);
     }
     sum += total.x + total.y;
+    if constexpr (LSE) exact += before.x + before.y;
   }
 
   // The weights of a whole key tile that every row of the warp sees, scales
@@ -740,7 +755,7 @@ struct Row {
       follow(ask ? high : -INFINITY, o_set);
     }
     const float shift = ref == -INFINITY ? 0.0f : -ref;
-    float2 u = make_float2(0.0f, 0.0f), v = make_float2(0.0f, 0.0f);
+    float2 u = make_float2(0.0f, 0.0f), before = u;
 #pragma unroll 1
     for (int c = 0; c < kKeys; c += 64) {  // P's columns overlay S's from the front: behind those read here
       float2 y[16];
@@ -748,12 +763,12 @@ struct Row {
       tmem_ld32(t, S + c + 32);
       tc_wait_ld(s, t);
       logits(y, s, gm + c, shift);
-      weights(y, S + c / 2, u);
+      weights(y, S + c / 2, u, before);
       logits(y, t, gm + c + 32, shift);
-      weights(y, S + c / 2 + 16, v);
+      weights(y, S + c / 2 + 16, u, before);
     }
-    u = add_f32x2(u, v);
     sum += u.x + u.y;
+    if constexpr (LSE) exact += before.x + before.y;
   }
 };
 
@@ -778,7 +793,7 @@ __device__ __forceinline__ void store32(const AttnArgs& a, int64_t at, const flo
   }
 }
 
-template <int D, int B>
+template <int D, int B, bool LSE>
 __device__ __forceinline__ bool softmax_role(const AttnArgs& a, const Place& place, unsigned char* sm, uint32_t bars,
                                              uint32_t tmem, int qt) {
   using Cfg = AttnCfg<D, B>;
@@ -786,7 +801,7 @@ __device__ __forceinline__ bool softmax_role(const AttnArgs& a, const Place& pla
   const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
   int8_t* exps = reinterpret_cast<int8_t*>(sm + Cfg::EXPS);
   const float* gam = reinterpret_cast<const float*>(sm + Cfg::GAM);
-  Row<D> row;
+  Row<D, LSE> row;
   row.S = tmem + lanes + qt * kKeys;
   row.O = tmem + lanes + 2 * kKeys + qt * D;
   int c = 0, ns = 0;
@@ -804,6 +819,7 @@ __device__ __forceinline__ bool softmax_role(const AttnArgs& a, const Place& pla
     if (there) limit = a.causal ? max(0, it.s.len - it.s.fresh + rr / a.g + 1) : it.s.len;
     row.ref = -INFINITY;
     row.sum = 0.0f;
+    row.exact = 0.0f;
     if (nt > 0) {
       if (two) {
         rotate_queries<D>(a, it, sm + Cfg::Q + qt * Cfg::TILE, exps + qt * 128, r0, 1024 / D, r0 + wr, -qt * 128, 1, 0, lane);
@@ -868,6 +884,7 @@ __device__ __forceinline__ bool softmax_role(const AttnArgs& a, const Place& pla
     if (!whole) {
       // rows, or row copies, for the join
       if (there) a.part_ml[slot * 256 + qt * 128 + warp * 32 + lane] = make_float2(row.ref, row.sum);
+      if (LSE && there) a.part_e[slot * 256 + qt * 128 + warp * 32 + lane] = row.exact;
       if (wr > 0) {
         float4* dst = a.part_o + slot * (D / 4) * 256 + qt * 128 + warp * 32 + lane;
 #pragma unroll 1
@@ -888,7 +905,7 @@ __device__ __forceinline__ bool softmax_role(const AttnArgs& a, const Place& pla
       if (wr > 0 && (two || qt == 0) && (two || warp * 32 < apart)) {
         const float sum = row.sum, inv = sum == 0.0f ? 0.0f : 1.0f / sum;
         const int64_t orow = out_row(x);
-        if (there && a.lse) a.lse[orow] = sum == 0.0f ? -INFINITY : (row.ref + log2f(sum)) * 0.6931471805599453f;
+        if (LSE && there) a.lse[orow] = sum == 0.0f ? -INFINITY : (row.ref + log2f(row.exact)) * 0.6931471805599453f;
 #pragma unroll 1
         for (int k = 0; k < D; k += 32) {
           uint32_t o[32];
@@ -907,17 +924,24 @@ __device__ __forceinline__ bool softmax_role(const AttnArgs& a, const Place& pla
       // the copies of each row: references and sums through shared memory (the second query tile is free), O scaled
       // to the common reference through this CTA's rows in the workspace, summed in a fixed order
       float2* ml = reinterpret_cast<float2*>(sm + Cfg::Q + Cfg::TILE);  // [2][128] of the copies, then [128] of the rows
+      float* before = reinterpret_cast<float*>(ml + 384);                   // their sums before rounding
       const int me = qt * 128 + warp * 32 + lane;
       ml[me] = there ? make_float2(row.ref, row.sum) : make_float2(-INFINITY, 0.0f);
+      if constexpr (LSE) before[me] = there ? row.exact : 0.0f;
       named_sync<1, 256>();
-      float top = -INFINITY, all = 0.0f;
+      float top = -INFINITY, all = 0.0f, exact = 0.0f;
       for (int k = 0; k < 2 * reps; ++k) top = fmaxf(top, ml[(k & 1) * 128 + (k >> 1) * apart + x].x);
       const float base = top == -INFINITY ? 0.0f : top;
       for (int k = 0; k < 2 * reps; ++k) {
         const float2 y = ml[(k & 1) * 128 + (k >> 1) * apart + x];
-        all = fmaf(ex2(y.x - base), y.y, all);
+        const float w = ex2(y.x - base);
+        all = fmaf(w, y.y, all);
+        if constexpr (LSE) exact = fmaf(w, before[(k & 1) * 128 + (k >> 1) * apart + x], exact);
       }
-      if (qt == 0 && warp * 32 < apart) ml[256 + x] = make_float2(top, all);
+      if (qt == 0 && warp * 32 < apart) {
+        ml[256 + x] = make_float2(top, all);
+        if constexpr (LSE) before[256 + x] = exact;
+      }
       float4* mine = a.copies + static_cast<int64_t>(blockIdx.x) * (D / 4) * 256;
       if (wr > 0) {
         const float keep = row.sum == 0.0f ? 0.0f : ex2(row.ref - base);
@@ -958,7 +982,7 @@ __device__ __forceinline__ bool softmax_role(const AttnArgs& a, const Place& pla
         else
           *reinterpret_cast<float4*>(static_cast<float*>(a.out) + orow * D + 4 * d) =
               make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-        if (a.lse && d == 0) a.lse[orow] = t.y == 0.0f ? -INFINITY : (t.x + log2f(t.y)) * 0.6931471805599453f;
+        if (LSE && d == 0) a.lse[orow] = t.y == 0.0f ? -INFINITY : (t.x + log2f(before[256 + y])) * 0.6931471805599453f;
       }
       named_sync<1, 256>();
     }
@@ -967,7 +991,7 @@ __device__ __forceinline__ bool softmax_role(const AttnArgs& a, const Place& pla
   return true;
 }
 
-template <int D, int B>
+template <int D, int B, bool LSE>
 __global__ void __launch_bounds__(512, 1) paged_attn_kernel(const __grid_constant__ AttnArgs a,
                                                             const __grid_constant__ CUtensorMap vmap) {
   using Cfg = AttnCfg<D, B>;
@@ -1025,7 +1049,7 @@ __global__ void __launch_bounds__(512, 1) paged_attn_kernel(const __grid_constan
   bool ok = true;
   if (place.count > 0) {
     if (warp < 8) {
-      ok = softmax_role<D, B>(a, place, sm, bars, tmem, warp >> 2);
+      ok = softmax_role<D, B, LSE>(a, place, sm, bars, tmem, warp >> 2);
     } else if (warp < 12) {
       ok = decode_role<D, B>(a, place, sm, base, bars);
     } else {
@@ -1062,7 +1086,7 @@ __global__ void __launch_bounds__(256) paged_attn_join(const __grid_constant__ A
   const int n = it.pieces * it.copies, nr = min(R, it.rows - r0);
   if (n == 0 || nr <= 0) return;
   __shared__ float2 s_ml[kJoin * 8][R];
-  __shared__ float s_red[8][R], s_ref[R], s_sum[R];
+  __shared__ float s_red[8][R], s_red_e[8][R], s_ref[R], s_sum[R], s_exact[R];
   __shared__ __align__(16) float s_out[G][R][D];
   const int lc = 31 - __clz(it.copies), apart = it.copies > 1 ? 256 / it.copies : 0;
   // entry e: copy c of piece k; CTA c0's piece lies in its second slot, those that go on with it use their first
@@ -1086,22 +1110,33 @@ __global__ void __launch_bounds__(256) paged_attn_join(const __grid_constant__ A
 #pragma unroll
   for (int w = 0; w < 8; ++w) top = fmaxf(top, s_red[w][r]);
   const float base = top == -INFINITY ? 0.0f : top;
-  float sum = 0.0f;
+  float sum = 0.0f, exact = 0.0f;
   if (r < nr)
     for (int e = tid / R; e < n; e += 256 / R) {  // its own entries
       const float w = ex2(s_ml[e][r].x - base);
       sum = fmaf(w, s_ml[e][r].y, sum);
+      if (a.lse) exact = fmaf(w, __ldcg(a.part_e + slot(e) * 256 + row(e) + r), exact);
       s_ml[e][r].x = w;
     }
 #pragma unroll
-  for (int o = R; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  for (int o = R; o < 32; o <<= 1) {
+    sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    exact += __shfl_xor_sync(0xffffffffu, exact, o);
+  }
   __syncthreads();
-  if ((tid & 31) < R) s_red[tid >> 5][r] = sum;
+  if ((tid & 31) < R) {
+    s_red[tid >> 5][r] = sum;
+    s_red_e[tid >> 5][r] = exact;
+  }
   __syncthreads();
   if (tid < R) {
-    float all = 0.0f;
-    for (int w = 0; w < 8; ++w) all += s_red[w][r];
+    float all = 0.0f, before = 0.0f;
+    for (int w = 0; w < 8; ++w) {
+      all += s_red[w][r];
+      before += s_red_e[w][r];
+    }
     s_sum[r] = all;
+    s_exact[r] = before;
     s_ref[r] = top;
   }
   const int d = tid / R % TPR, g = tid / (R * TPR);
@@ -1136,7 +1171,7 @@ __global__ void __launch_bounds__(256) paged_attn_join(const __grid_constant__ A
     else
       *reinterpret_cast<float4*>(static_cast<float*>(a.out) + orow * D + x) =
           make_float4(v.x * inv, v.y * inv, v.z * inv, v.w * inv);
-    if (a.lse && x == 0) a.lse[orow] = all == 0.0f ? -INFINITY : (s_ref[q] + log2f(all)) * 0.6931471805599453f;
+    if (a.lse && x == 0) a.lse[orow] = all == 0.0f ? -INFINITY : (s_ref[q] + log2f(s_exact[q])) * 0.6931471805599453f;
   }
 }
 
@@ -1173,17 +1208,21 @@ static bool encode_v_map(CUtensorMap* m, const octo_pages* p, int D, int box) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int B>
+template <int D, int B, bool LSE>
 static cudaError_t launch_attn(const AttnArgs& a, const CUtensorMap& map, int ctas, cudaStream_t st) {
   static LaunchCache cache;
   int resident = 0;
-  cudaError_t e = launch_setup(paged_attn_kernel<D, B>, cache, 512, AttnCfg<D, B>::SMEM, resident);
+  cudaError_t e = launch_setup(paged_attn_kernel<D, B, LSE>, cache, 512, AttnCfg<D, B>::SMEM, resident);
   if (e != cudaSuccess) return e;
-  paged_attn_kernel<D, B><<<ctas, 512, AttnCfg<D, B>::SMEM, st>>>(a, map);
+  paged_attn_kernel<D, B, LSE><<<ctas, 512, AttnCfg<D, B>::SMEM, st>>>(a, map);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const unsigned groups = static_cast<unsigned>((std::min<int64_t>(a.n_rows * a.g, kRows) + kJoinRows - 1) / kJoinRows);
   paged_attn_join<D><<<dim3(ctas, groups), 256, 0, st>>>(a);
   return cudaGetLastError();
+}
+template <int D, int B>
+static cudaError_t launch_lse(const AttnArgs& a, const CUtensorMap& map, int ctas, cudaStream_t st) {
+  return a.lse ? launch_attn<D, B, true>(a, map, ctas, st) : launch_attn<D, B, false>(a, map, ctas, st);
 }
 
 }  // namespace paged
@@ -1194,7 +1233,7 @@ extern "C" size_t octo_paged_attn_workspace(const octo_layout* L, int64_t n_rows
   if (check_layout(L) != OCTO_OK || L->d > 128 || n_rows < 0 || n_seqs < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0)
     return 0;
   // two partial slots and the row copies of each CTA, whatever the sizes
-  return attn_ctas() * (3 * 256 * L->d * sizeof(float) + 2 * 256 * sizeof(float2) + sizeof(Shared));
+  return attn_ctas() * (3 * 256 * L->d * sizeof(float) + 2 * 256 * (sizeof(float2) + sizeof(float)) + sizeof(Shared));
 }
 
 extern "C" int octo_paged_attn(const octo_layout* L, const octo_tables* tab, const octo_pages* pages,
@@ -1248,7 +1287,8 @@ extern "C" int octo_paged_attn(const octo_layout* L, const octo_tables* tab, con
   a.part_o = static_cast<float4*>(workspace);
   a.copies = a.part_o + static_cast<size_t>(2) * ctas * (L->d / 4) * 256;
   a.part_ml = reinterpret_cast<float2*>(a.copies + static_cast<size_t>(ctas) * (L->d / 4) * 256);
-  a.shared = reinterpret_cast<Shared*>(a.part_ml + static_cast<size_t>(2) * ctas * 256);
+  a.part_e = reinterpret_cast<float*>(a.part_ml + static_cast<size_t>(2) * ctas * 256);
+  a.shared = reinterpret_cast<Shared*>(a.part_e + static_cast<size_t>(2) * ctas * 256);
   const int qe = q_dtype == OCTO_BF16 ? 2 : 4;
   a.q_vec = reinterpret_cast<uintptr_t>(q) % 16 == 0 && q_row_stride * qe % 16 == 0 && q_head_stride * qe % 16 == 0;
   // V comes in boxes that lie inside one page: the largest power of two (8-row swizzle groups) that divides it
@@ -1259,8 +1299,8 @@ extern "C" int octo_paged_attn(const octo_layout* L, const octo_tables* tab, con
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (L->d == 64)
-    e = L->b == 2 ? launch_attn<64, 2>(a, map, ctas, st) : L->b == 3 ? launch_attn<64, 3>(a, map, ctas, st) : launch_attn<64, 4>(a, map, ctas, st);
+    e = L->b == 2 ? launch_lse<64, 2>(a, map, ctas, st) : L->b == 3 ? launch_lse<64, 3>(a, map, ctas, st) : launch_lse<64, 4>(a, map, ctas, st);
   else
-    e = L->b == 2 ? launch_attn<128, 2>(a, map, ctas, st) : L->b == 3 ? launch_attn<128, 3>(a, map, ctas, st) : launch_attn<128, 4>(a, map, ctas, st);
+    e = L->b == 2 ? launch_lse<128, 2>(a, map, ctas, st) : L->b == 3 ? launch_lse<128, 3>(a, map, ctas, st) : launch_lse<128, 4>(a, map, ctas, st);
   return e == cudaSuccess ? OCTO_OK : OCTO_ECUDA;
 }

@@ -8,7 +8,10 @@ Error bounds that the tests use, u = eps / 2 of a type (bf16 2^-8, fp16 2^-11, f
   2^-24 * sqrt(d) * |scale| * gamma * max|q~| (fp16 subnormals below the row's power of two, |u| <= 1) plus the fp32
   accumulation, 4 d * 2^-24 of the sum of magnitudes. Weights are then off by a factor in exp(+-2 Dmax) (numerator and
   denominator), and by u(bf16) = 2^-8 from rounding the weight: |out - ref| <= (expm1(2 Dmax) + 2^-8 + 2^-16) * sum p |v|
-  + u(out) |ref|; |lse - ref| <= Dmax + 2^-20 (1 + |ref|).
+  + u(out) |ref|; |lse - ref| <= Dmax + 2^-20 (1 + |ref|). The row sum is that of the rounded weights p (1 + e), |e| <=
+  u / (1 + u) (half a step against a value that is at least one step above a power of two): out - ref = sum p e (v - ref)
+  / (1 + sum p e), which is at most max|e| / (1 - max|e|) = u times sum p |v - ref|, with |v - ref| <= |v| + |ref| and
+  |ref| <= sum p |v|. So the bound on the weights' rounding is 2^-8 * (sum p |v| + |ref|).
 * a logit of ``paged_mass`` comes from hi + lo pairs, high parts on grids of 2^-11 (queries, scaled so that their row's
   largest is below 1 and at least 1/2: units of it cost a factor 2) and 2^-12 (keys): the dropped product is at most
   2^-12 * 2^-13 per term, d terms; the low parts round by 2^-23 and 2^-24, against sum |u| <= sqrt(d) and |q~|; the fp32
@@ -129,7 +132,7 @@ def attn(pool, q, cu, causal=True, scale=None):
 
 def check_attn(out, ref, mag, dmax, bf16):
     got = out.float().cpu().numpy().astype(np.float64)
-    tol = (np.expm1(2 * dmax)[..., None] + 2.0 ** -8 + 2.0 ** -16) * mag + (2.0 ** -8 * np.abs(ref) if bf16 else 0)
+    tol = (np.expm1(2 * dmax)[..., None] + 2.0 ** -8 + 2.0 ** -16) * mag + 2.0 ** -8 * np.abs(ref) * (2 if bf16 else 1)
     err = np.abs(got - ref)
     assert np.isfinite(got).all(), "outputs are not finite"
     bad = err > tol
