@@ -14,12 +14,14 @@ host does not: what they find wrong goes to the cache's status word (:meth:`Page
 
 As the whole binding, this module only marshals arguments; shapes, types and devices that plain pointers hide from the C
 ABI are refused with ValueError. Calls run on the tensors' device, on ``stream`` or torch's current stream there; tensors
-used on a stream other than the one they were made on need ``record_stream`` as in any torch program.
+used on a stream other than the one they were made on need ``record_stream`` as in any torch program. What a call with
+``stream`` allocates (outputs, scratch) is made on that stream.
 """
 
 from __future__ import annotations
 
 import ctypes
+import functools
 from dataclasses import dataclass
 
 import numpy as np
@@ -47,6 +49,18 @@ def _on(index: int, stream, call):
         return call(_raw_stream(index) if stream is None else stream.cuda_stream)
     with torch.cuda.device(index):
         return call(_raw_stream(index) if stream is None else stream.cuda_stream)
+
+
+def _on_its_stream(f):
+    """With ``stream``, f runs with it current: what f allocates or fills belongs to the stream that uses it."""
+    @functools.wraps(f)
+    def call(*args, **kw):
+        stream = kw.get("stream")
+        if stream is None:
+            return f(*args, **kw)
+        with torch.cuda.stream(stream):
+            return f(*args, **kw)
+    return call
 
 
 def _same_device(index: int, *tensors):
@@ -106,6 +120,7 @@ def _rope_pair(x: torch.Tensor, y: torch.Tensor | None, what: str):
     return y, _lib.OctoRopeTensor(x.data_ptr(), y.data_ptr(), x.shape[1], sx[0], sx[1], sy[0], sy[1])
 
 
+@_on_its_stream
 def rope(q: torch.Tensor, positions: torch.Tensor, table: RopeTable, k: torch.Tensor | None = None,
          interleaved: bool = False, inverse: bool = False, out: torch.Tensor | None = None,
          k_out: torch.Tensor | None = None, stream=None):
@@ -276,6 +291,7 @@ def paged_write(layout: api.Layout, staged: api.Cache, V: torch.Tensor | None, c
     return cache
 
 
+@_on_its_stream
 def paged_append(layout: api.Layout, tables: api.DeviceTables, keys: torch.Tensor, V: torch.Tensor | None,
                  cache: PagedCache, page_table: torch.Tensor, starts: torch.Tensor, cu: torch.Tensor,
                  staged: api.Cache | None = None, stream=None) -> PagedCache:
@@ -336,6 +352,7 @@ def _scratch(workspace, need: int, cache: PagedCache):
     return workspace.buf
 
 
+@_on_its_stream
 def paged_attn(layout: api.Layout, tables: api.DeviceTables, q: torch.Tensor, cache: PagedCache, page_table: torch.Tensor,
                seq_lens: torch.Tensor, cu_q: torch.Tensor | None = None, causal: bool = True, scale: float | None = None,
                dtype=None, out: torch.Tensor | None = None, lse=None, workspace: api.Workspace | None = None, stream=None):
@@ -343,7 +360,8 @@ def paged_attn(layout: api.Layout, tables: api.DeviceTables, q: torch.Tensor, ca
 
     q [rows][Hq][d] (float32 or bfloat16): rows cu_q[i] .. cu_q[i+1] - 1 (cu_q int32 [B + 1]; None: the same number for
     each) are the last tokens of sequence i, whose cache holds seq_lens[i] slots. With ``causal`` each new token sees the
-    slots up to its own, else all of its sequence. A row that sees nothing gives 0 (lse -inf). Returns out [rows][Hq][d]
+    slots up to its own, else all of its sequence. A row that sees nothing gives 0 (lse -inf). Values of slots that one row
+    of a sequence sees must be finite for its other rows too. Returns out [rows][Hq][d]
     (``dtype`` float32 or bfloat16, by default q's), and with ``lse`` (True, or a float32 [rows][Hq] tensor) the pair
     (out, lse) with lse = ln sum exp(scale * logits).
 
@@ -354,6 +372,8 @@ def paged_attn(layout: api.Layout, tables: api.DeviceTables, q: torch.Tensor, ca
         out = torch.empty(q.shape, dtype=q.dtype if dtype is None else dtype, device=q.device)
     elif out.shape != q.shape or not out.is_contiguous() or dtype not in (None, out.dtype):
         raise ValueError(f"out must be a contiguous {tuple(q.shape)} tensor")
+    elif q.numel() and out.data_ptr() < _end(q) and q.data_ptr() < _end(out):
+        raise ValueError("out must not overlap q")
     odt = _DTYPES.get(out.dtype)
     if odt is None:
         raise ValueError(f"unsupported output dtype {out.dtype}")
@@ -381,6 +401,7 @@ def paged_attn(layout: api.Layout, tables: api.DeviceTables, q: torch.Tensor, ca
     return out if lse is None else (out, lse)
 
 
+@_on_its_stream
 def paged_mass(layout: api.Layout, tables: api.DeviceTables, q: torch.Tensor, lse: torch.Tensor, cache: PagedCache,
                page_table: torch.Tensor, seq_lens: torch.Tensor, mass: torch.Tensor, cu_q: torch.Tensor | None = None,
                causal: bool = True, scale: float | None = None, decay: float = 1.0, out: torch.Tensor | None = None,
@@ -417,6 +438,7 @@ def paged_mass(layout: api.Layout, tables: api.DeviceTables, q: torch.Tensor, ls
     return out
 
 
+@_on_its_stream
 def paged_evict(layout: api.Layout, cache: PagedCache, page_table: torch.Tensor, seq_lens: torch.Tensor,
                 mass: torch.Tensor, keep: int, dst_table: torch.Tensor, sink: int = 0, recent: int = 0,
                 dst: PagedCache | None = None, kept: torch.Tensor | None = None, new_lens: torch.Tensor | None = None,

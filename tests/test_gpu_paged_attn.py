@@ -251,3 +251,30 @@ def test_two_streams_with_a_workspace_each(cuda_ok):
             paged.paged_attn(*args, out=outs[s][k], workspace=ws[s], stream=streams[s])
     torch.cuda.synchronize()
     assert all(torch.equal(o, want) for s in outs for o in s)
+
+
+def test_a_call_on_another_stream_owns_what_it_allocates(cuda_ok):
+    """cu_q, scratch and outputs of a call with ``stream`` are made on that stream: neither a busy current stream nor one
+    that reuses the memory at once reaches them. Appending tokens likewise."""
+    pool = pr.Pool(27, 128, 3, 64, 2, [3000, 64])
+    q = torch.from_numpy(_queries(28, 16, 8, 128)).to(torch.bfloat16).cuda()
+    args = (pool.lay, pool.tables, q, pool.cache, pool.page_table, pool.seq_lens)
+    want = paged.paged_attn(*args)
+    keys = torch.randn(8, 2, 128, device="cuda", generator=torch.Generator("cuda").manual_seed(3))
+    V = keys.to(torch.bfloat16)
+    table = torch.arange(2, dtype=torch.int32, device="cuda").view(2, 1)
+    starts, cu = torch.tensor([3, 9], dtype=torch.int32, device="cuda"), torch.tensor([0, 5, 8], dtype=torch.int32, device="cuda")
+    pools = [paged.PagedCache.empty(pool.lay, 2, 2, 64) for _ in range(2)]
+    paged.paged_append(pool.lay, pool.tables, keys, V, pools[0], table, starts, cu)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)  # the current stream is busy for some ten milliseconds
+    out = paged.paged_attn(*args, stream=side)
+    paged.paged_append(pool.lay, pool.tables, keys, V, pools[1], table, starts, cu, stream=side)
+    junk = [torch.full((1 << k,), float("nan"), device="cuda") for k in range(10, 25)]
+    side.synchronize()
+    assert torch.equal(out, want)
+    torch.cuda.synchronize()
+    for a, b in ((pools[0].packed, pools[1].packed), (pools[0].gamma, pools[1].gamma), (pools[0].V, pools[1].V)):
+        assert torch.equal(a, b)
+    del junk

@@ -256,3 +256,12 @@ def test_rope_binding_refuses():
         paged.rope(buf[:256].view(4, 2, 32), p, t, out=buf[32:].view(4, 2, 32))
     with pytest.raises(_lib.OctoError):
         paged.RopeTable((16,), theta=0.1, device="cpu")
+
+
+def test_attn_refuses_an_output_over_its_queries():
+    lay, tabs, c = _cpu()
+    buf = torch.zeros(5 * 4 * 64)
+    for at in (0, 64):
+        with pytest.raises(ValueError, match="overlap"):
+            paged.paged_attn(lay, tabs, buf[:1024].view(4, 4, 64), c, _i32([[0, 1], [2, 3]]), _i32([5, 6]),
+                             out=buf[at:at + 1024].view(4, 4, 64))
