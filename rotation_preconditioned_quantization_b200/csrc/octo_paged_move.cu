@@ -139,7 +139,6 @@ struct SelectArgs {
   int64_t mass_stride;
   int n_heads, cap, keep, sink, recent;
   int32_t* kept;
-  int32_t* new_lens;
   float* new_mass;
   int32_t* status;
 };
@@ -184,10 +183,7 @@ __global__ void __launch_bounds__(1024) paged_select_kernel(const __grid_constan
   const int row = blockIdx.x / C, i = row / a.n_heads, h = row % a.n_heads;
   const int told = a.seq_lens[i];
   const int n = min(max(told, 0), a.cap);
-  if (tid == 0 && h == 0 && rank_in == 0) {
-    a.new_lens[i] = min(n, a.keep);
-    if (n != told) report(a.status, OCTO_PAGED_BAD_LENGTH);
-  }
+  if (tid == 0 && h == 0 && rank_in == 0 && n != told) report(a.status, OCTO_PAGED_BAD_LENGTH);
   const float* mass = a.mass + static_cast<int64_t>(row) * a.mass_stride;
   int32_t* kept = a.kept + static_cast<int64_t>(row) * a.keep;
   float* out = a.new_mass ? a.new_mass + static_cast<int64_t>(row) * a.keep : nullptr;
@@ -356,7 +352,9 @@ struct GatherArgs {
   Table src, dst;
   MoveArgs m;
   const int32_t* kept;
-  int keep;
+  int keep, cap;
+  const int32_t* seq_lens;
+  int32_t* new_lens;  // may be seq_lens: written here, when the choice has read all lengths
 };
 
 template <int TILE>
@@ -364,6 +362,8 @@ __global__ void __launch_bounds__(256) paged_gather_kernel(const __grid_constant
   __shared__ int64_t s_src[TILE], s_srow[TILE], s_vsrc[TILE], s_dst[TILE], s_page[TILE];
   const int i = blockIdx.y / a.src.n_heads, h = blockIdx.y % a.src.n_heads, P = a.src.page_size;
   const int k0 = blockIdx.x * TILE, nt = min(TILE, a.keep - k0);
+  if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0)
+    a.new_lens[i] = min(min(max(static_cast<int>(load_now(a.seq_lens + i)), 0), a.cap), a.keep);
   for (int t = threadIdx.x; t < nt; t += 256) {
     const int slot = __ldg(a.kept + static_cast<int64_t>(blockIdx.y) * a.keep + k0 + t);
     int64_t from = kNone, to = kNone, row = kNone, page = 0;
@@ -441,6 +441,11 @@ extern "C" int octo_paged_evict(const octo_layout* L, const octo_pages* src, con
   if (rows > 65535) return OCTO_EUNSUPPORTED;  // grid.y limit
   if (rows == 0) return OCTO_OK;
   if (!seq_lens || !mass || !kept || !new_lens) return OCTO_EINVAL;
+  if (new_mass) {  // the choice writes it while it reads mass
+    const uintptr_t m0 = reinterpret_cast<uintptr_t>(mass), o0 = reinterpret_cast<uintptr_t>(new_mass);
+    if (o0 < m0 + static_cast<uintptr_t>(rows) * mass_stride * 4 && m0 < o0 + static_cast<uintptr_t>(rows) * keep * 4)
+      return OCTO_EINVAL;
+  }
   SelectArgs s{};
   s.seq_lens = seq_lens;
   s.mass = mass;
@@ -451,7 +456,6 @@ extern "C" int octo_paged_evict(const octo_layout* L, const octo_pages* src, con
   s.sink = sink;
   s.recent = recent;
   s.kept = kept;
-  s.new_lens = new_lens;
   s.new_mass = new_mass;
   s.status = src->status;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -467,6 +471,9 @@ extern "C" int octo_paged_evict(const octo_layout* L, const octo_pages* src, con
                  dst->gamma,  static_cast<uint4*>(dst->V), L->words, src->page_size, L->d / 8};
   g.kept = kept;
   g.keep = keep;
+  g.cap = s.cap;
+  g.seq_lens = seq_lens;
+  g.new_lens = new_lens;
   constexpr int TILE = 128;
   paged_gather_kernel<TILE><<<dim3((keep + TILE - 1) / TILE, static_cast<unsigned>(rows)), 256, 0, st>>>(g);
   return cudaGetLastError() == cudaSuccess ? OCTO_OK : OCTO_ECUDA;

@@ -448,7 +448,7 @@ def paged_evict(layout: api.Layout, cache: PagedCache, page_table: torch.Tensor,
     ``dst``, by default the same pool; pages written must not hold tokens that the call reads). Sequences of at most
     ``keep`` slots move whole. mass float32 [B][heads][slots].
 
-    Returns (new_lens int32 [B], kept int32 [B][heads][keep]: the slots kept, -1 behind the last; new_mass float32
+    Returns (new_lens int32 [B], which may be given as seq_lens itself; kept int32 [B][heads][keep]: the slots kept, -1 behind the last; new_mass float32
     [B][heads][keep], 0 behind the last). Kept tokens keep the positions that their keys were rotated by.
     """
     _check_pool(layout, cache, False)
@@ -474,6 +474,8 @@ def paged_evict(layout: api.Layout, cache: PagedCache, page_table: torch.Tensor,
         new_mass = torch.empty((B, H, keep), dtype=_F32, device=dev)
     else:
         _dense(new_mass, "new_mass", _F32, (B, H, keep))
+        if mass.numel() and new_mass.data_ptr() < _end(mass) and mass.data_ptr() < _end(new_mass):
+            raise ValueError("new_mass must not overlap mass")
     t, z = _table(page_table, B), _table(dst_table, B, "dst_table")
     _same_device(index, page_table, seq_lens, mass, dst_table, dst.packed, kept, new_lens, new_mass)
     st = _on(index, stream, lambda s: _lib.lib().octo_paged_evict(

@@ -258,3 +258,30 @@ def test_evict_graph_replay(cuda_ok):
         for h in range(2):
             s = pr.select(mass[0, h].cpu().numpy(), n, 20, 1, 2)
             assert kept[0, h, :len(s)].cpu().numpy().tolist() == s.tolist() and int(nl[0]) == len(s)
+
+
+@pytest.mark.parametrize("slots,heads", [(600, 24), (9000, 40)])
+def test_evict_lengths_in_place(cuda_ok, slots, heads):
+    """new_lens given as seq_lens: every head is cut by the lengths of before."""
+    lay = api.Layout(64, 2)
+    lens = [slots, slots - 77, 5, 0]
+    per, keep = -(-slots // 16), 100
+    cache = paged.PagedCache.empty(lay, 4 * (per + 7), heads, 16, values=False)
+    cache.gamma.copy_(torch.rand(cache.gamma.shape, generator=torch.Generator().manual_seed(1)))
+    table = torch.arange(4 * per, dtype=torch.int32, device="cuda").view(4, per)
+    dst = (4 * per + torch.arange(28, dtype=torch.int32, device="cuda")).view(4, 7)
+    mass = torch.rand(4, heads, slots, generator=torch.Generator().manual_seed(2)).cuda()
+    want = paged.paged_evict(lay, cache, table, _i32(lens), mass, keep, dst, sink=2, recent=9)
+    moved = cache.gamma[4 * per:].clone()
+    for _ in range(5):
+        cache.gamma[4 * per:] = -1.0
+        now = _i32(lens)
+        got = paged.paged_evict(lay, cache, table, now, mass, keep, dst, sink=2, recent=9, new_lens=now)
+        assert got[0] is now and now.tolist() == [min(n, keep) for n in lens]
+        assert torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
+        for i, n in enumerate(lens):
+            n = min(n, keep)
+            rows = dst[i].long() - 4 * per
+            a, b = (x[rows].transpose(0, 1).reshape(heads, -1)[:, :n] for x in (cache.gamma[4 * per:], moved))
+            assert torch.equal(a, b)
+    cache.check()

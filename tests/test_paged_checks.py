@@ -265,3 +265,11 @@ def test_attn_refuses_an_output_over_its_queries():
         with pytest.raises(ValueError, match="overlap"):
             paged.paged_attn(lay, tabs, buf[:1024].view(4, 4, 64), c, _i32([[0, 1], [2, 3]]), _i32([5, 6]),
                              out=buf[at:at + 1024].view(4, 4, 64))
+
+
+def test_evict_refuses_a_new_mass_over_the_mass():
+    lay, _, c = _cpu()
+    buf = torch.zeros(2 * 2 * 32 + 16)
+    with pytest.raises(ValueError, match="overlap"):
+        paged.paged_evict(lay, c, _i32([[0, 1], [2, 3]]), _i32([5, 6]), buf[:128].view(2, 2, 32), 16,
+                          _i32([[0, 1], [2, 3]]), new_mass=buf[64:128].view(2, 2, 16))
