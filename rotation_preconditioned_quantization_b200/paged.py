@@ -113,6 +113,8 @@ def _rope_pair(x: torch.Tensor, y: torch.Tensor | None, what: str):
         sy = y.stride()
         if y.shape != x.shape or y.dtype is not x.dtype:
             raise ValueError(f"{what} must have its input's shape and type")
+        if any(s == 0 and n > 1 for n, s in zip(y.shape, sy)):
+            raise ValueError(f"{what} must not be an expanded view")
         if (y.data_ptr() != x.data_ptr() or sx != sy) and x.numel() and y.data_ptr() < _end(x) and x.data_ptr() < _end(y):
             raise ValueError(f"{what} must be the input itself or not overlap it")
     if (sx[2] != 1 or sy[2] != 1) and x.shape[2] > 1:
@@ -139,6 +141,8 @@ def rope(q: torch.Tensor, positions: torch.Tensor, table: RopeTable, k: torch.Te
     if positions.dtype is not _I32 or positions.shape != (axes, n) or (n > 1 and positions.stride(1) != 1):
         raise ValueError(f"positions must be int32 [{axes}][{n}], contiguous in its last dimension, got "
                          f"{positions.dtype} {tuple(positions.shape)}")
+    if axes > 1 and positions.stride(0) < n:
+        raise ValueError("positions must not be an expanded view: its rows overlap")
     out, a = _rope_pair(q, out, "out")
     b = None
     if k is not None:
@@ -250,6 +254,8 @@ def _table(page_table: torch.Tensor, B: int, what: str = "page_table"):
     s0, s1 = page_table.stride()
     if s1 != 1 and n > 1:
         raise ValueError(f"{what} must be contiguous in its last dimension")
+    if B > 1 and s0 < n:
+        raise ValueError(f"{what} must not be an expanded view: its rows overlap")
     return _lib.OctoPageTable(page_table.data_ptr(), s0 if s0 > n else n, B, n)
 
 

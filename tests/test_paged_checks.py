@@ -273,3 +273,18 @@ def test_evict_refuses_a_new_mass_over_the_mass():
     with pytest.raises(ValueError, match="overlap"):
         paged.paged_evict(lay, c, _i32([[0, 1], [2, 3]]), _i32([5, 6]), buf[:128].view(2, 2, 32), 16,
                           _i32([[0, 1], [2, 3]]), new_mass=buf[64:128].view(2, 2, 16))
+
+
+def test_expanded_views_are_refused():
+    """One row read as many has no stride that the C ABI can take: it would be read beyond its end."""
+    lay, tabs, c = _cpu()
+    q, lens = torch.zeros(4, 4, 64), _i32([5, 6])
+    with pytest.raises(ValueError, match="page_table must not be an expanded"):
+        paged.paged_attn(lay, tabs, q, c, _i32([[0, 1]]).expand(2, 2), lens)
+    with pytest.raises(ValueError, match="dst_table must not be an expanded"):
+        paged.paged_evict(lay, c, _i32([[0, 1], [2, 3]]), lens, torch.zeros(2, 2, 32), 16, _i32([[0, 1]]).expand(2, 2))
+    t = paged.RopeTable((4, 4), device="cpu")
+    with pytest.raises(ValueError, match="positions must not be an expanded"):
+        paged.rope(q, torch.zeros(1, 4, dtype=torch.int32).expand(2, 4), t)
+    with pytest.raises(ValueError, match="out must not be an expanded"):
+        paged.rope(q, torch.zeros(2, 4, dtype=torch.int32), t, out=torch.zeros(4, 1, 64).expand(4, 4, 64))
