@@ -123,26 +123,29 @@ __device__ __forceinline__ void bar_arrive(uint32_t bar) {
 __device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
-// Waits for the phase of this parity; false when it did not end within the
-// limit (about a second of polls), and then the caller gives up.
+__device__ __forceinline__ uint32_t bar_poll(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok;
+}
+// Waits for the phase of this parity, a whole warp; false when it did not end
+// within the limit (about a second of polls), and then the caller gives up.
+// All lanes get one answer: lanes that went on without the others would wait
+// for them at the warp's next collective instruction, which has no limit. So
+// lanes that ran out poll once more: if another lane of the warp saw the phase
+// end, they see it now (it stays ended until this warp arrives somewhere
+// again), and else they are the whole warp and agree.
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity) {
 #pragma unroll 1
-  for (int it = 0; it < (1 << 22); ++it) {
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    if (ok) return true;
-  }
-  return false;
+  for (int it = 0; it < (1 << 22); ++it)
+    if (bar_poll(bar, parity)) return true;
+  return __any_sync(__activemask(), bar_poll(bar, parity));
 }
 __device__ __forceinline__ void fence_async_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-template <int ID, int N>
-__device__ __forceinline__ void named_sync() {
-  asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(N) : "memory");
-}
 
 // ---- TMA --------------------------------------------------------------------
 __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {

@@ -240,13 +240,13 @@ struct AttnCfg {
   static constexpr int Q = 0, KT = 2 * TILE, V = 4 * TILE, TAB = 6 * TILE, RHO = TAB + (NE << SH);
   static constexpr int GAM = RHO + (QUAD ? 8 * 8 * 4 : 0), GMAX = GAM + GS * kKeys * 4, EXPS = GMAX + GS * 16,
                        BARS = EXPS + 256;
-  static constexpr int PLACE = BARS + 144, TMEM = PLACE + 40, DIR = PLACE + 48, RHOF = DIR + 128, SMEM = RHOF + 32;
+  static constexpr int PLACE = BARS + 18 * 8, TMEM = PLACE + 40, DIR = PLACE + 48, RHOF = DIR + 128, SMEM = RHOF + 32;
   static_assert(SMEM <= 232448, "shared memory of an SM");
   static constexpr int THREADS = 512;
 };
 
 // barriers
-enum { kQF = 0, kSF = 2, kPR = 4, kKF = 6, kKE = 8, kVF = 10, kVE = 12, kVZ = 14, kEND = 16, kBars = 17 };
+enum { kQF = 0, kSF = 2, kPR = 4, kKF = 6, kKE = 8, kVF = 10, kVE = 12, kVZ = 14, kEND = 16, kMEET = 17, kBars = 18 };
 
 __device__ __forceinline__ uint32_t bf16_pair(float x, float y) {
   const __nv_bfloat162 b2 = __floats2bfloat162_rn(x, y);
@@ -811,7 +811,16 @@ __device__ __forceinline__ bool softmax_role(const AttnArgs& a, const Place& pla
   Row<D, LSE> row;
   row.S = tmem + lanes + qt * kKeys;
   row.O = tmem + lanes + 2 * kKeys + qt * D;
-  int c = 0, ns = 0;
+  int c = 0;
+  uint32_t phase = 0;  // bit 0: of kSF, bit 1: of kMEET
+  // All softmax warps meet here. Not at a hardware barrier, which has no limit: a warp whose other waits ran out has left,
+  // and those that wait for it have to leave too.
+  auto meet = [&] {
+    __syncwarp();
+    if (lane == 0) bar_arrive(bars + 8 * kMEET);
+    phase ^= 2u;
+    return bar_wait(bars + 8 * kMEET, (phase >> 1) ^ 1u);
+  };
   for (Walk it(a, place); it.on(); it.next()) {
     const int nt = it.work(), rows = it.rows(), reps = it.reps();
     const bool two = reps == 0;
@@ -833,7 +842,7 @@ __device__ __forceinline__ bool softmax_role(const AttnArgs& a, const Place& pla
         __syncwarp();
       } else {
         rotate_queries<D>(a, it, sm + Cfg::Q, exps, (qt * 4 + warp) * (1024 / D), 8 * (1024 / D), rows, 0, reps, apart, lane);
-        named_sync<1, 256>();
+        if (!meet()) return false;
       }
       fence_async_shared();
       bar_arrive(bars + 8 * (kQF + qt));
@@ -841,8 +850,8 @@ __device__ __forceinline__ bool softmax_role(const AttnArgs& a, const Place& pla
       row.up = ldexpf(1.0f, ex);
       const bool plain = __all_sync(0xffffffffu, ex == 0);
       for (int j = two ? 0 : qt; j < nt; j += two ? 1 : 2) {
-        if (!bar_wait(bars + 8 * (kSF + qt), ns & 1)) return false;
-        ++ns;
+        if (!bar_wait(bars + 8 * (kSF + qt), phase & 1)) return false;
+        phase ^= 1u;
         tc_after();
         if (wr > 0) {  // a warp without rows leaves its part of P as it is: those rows go nowhere
           const float* gm = gam + ((c + j) % Cfg::GS) * kKeys;
@@ -868,8 +877,8 @@ __device__ __forceinline__ bool softmax_role(const AttnArgs& a, const Place& pla
         tc_before();
         bar_arrive(bars + 8 * (kPR + qt));
       }
-      if (!bar_wait(bars + 8 * (kSF + qt), ns & 1)) return false;  // O is complete
-      ++ns;
+      if (!bar_wait(bars + 8 * (kSF + qt), phase & 1)) return false;  // O is complete
+      phase ^= 1u;
       tc_after();
     }
     c += nt;
@@ -935,7 +944,7 @@ __device__ __forceinline__ bool softmax_role(const AttnArgs& a, const Place& pla
       const int me = qt * 128 + warp * 32 + lane;
       ml[me] = there ? make_float2(row.ref, row.sum) : make_float2(-INFINITY, 0.0f);
       if constexpr (LSE) before[me] = there ? row.exact : 0.0f;
-      named_sync<1, 256>();
+      if (!meet()) return false;
       float top = -INFINITY, all = 0.0f, exact = 0.0f;
       for (int k = 0; k < 2 * reps; ++k) top = fmaxf(top, ml[(k & 1) * 128 + (k >> 1) * apart + x].x);
       const float base = top == -INFINITY ? 0.0f : top;
@@ -967,7 +976,7 @@ __device__ __forceinline__ bool softmax_role(const AttnArgs& a, const Place& pla
           }
         }
       }
-      named_sync<1, 256>();
+      if (!meet()) return false;
       // threads along four rows, so that reads and writes both meet in sectors
       const int tid = threadIdx.x & 255, y0 = tid & 3;
       for (int e = tid >> 2; e < (rows + 3) / 4 * (D / 4); e += 64) {
@@ -991,7 +1000,7 @@ __device__ __forceinline__ bool softmax_role(const AttnArgs& a, const Place& pla
               make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
         if (LSE && d == 0) a.lse[orow] = t.y == 0.0f ? -INFINITY : (t.x + log2f(before[256 + y])) * 0.6931471805599453f;
       }
-      named_sync<1, 256>();
+      if (!meet()) return false;
     }
     tc_before();
   }
@@ -1025,6 +1034,7 @@ __global__ void __launch_bounds__(512, 1) paged_attn_kernel(const __grid_constan
       bar_init(bars + 8 * (kVZ + q), 32);
     }
     bar_init(bars + 8 * kEND, 1);
+    bar_init(bars + 8 * kMEET, 8);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == 12) tmem_alloc(s32(&s_tmem), 512);
