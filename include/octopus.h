@@ -410,7 +410,9 @@ OCTO_API int octo_paged_write(const octo_layout* L, const octo_pages* pages, con
  *   lse  device fp32 [n_rows][Hq] ln sum exp(logits), or NULL.
  *   workspace  device, 256-byte aligned, octo_paged_attn_workspace() bytes of
  *        scratch; nothing in it needs to be kept or cleared between calls.
- *        Calls that share it must not overlap on the GPU.
+ *        It may be octo_decode_attn's workspace too: bytes [0, 262400), the
+ *        front where that call keeps its status word and counters, are left
+ *        alone. Calls that share it must not overlap on the GPU.
  * Keys and queries enter the tensor cores as fp16 (queries scaled by a power
  * of two per row), weights and V as bf16; sums and softmax statistics are
  * fp32 (out is divided by the sum of the rounded weights, lse is that of the

@@ -233,7 +233,8 @@ def decode_attn_workspace_bytes(layout: Layout, B: int, Hq: int, Hkv: int, Lq: i
 
 class Workspace:
     """Device workspace for decode_attn: status word, ticket counters (zeroed
-    here, left zero by every completed call) and split partials."""
+    here, left zero by every completed call) and split partials. The paged
+    calls, whose scratch lies behind status and counters, take one as well."""
 
     def __init__(self, nbytes: int, device="cuda"):
         n = max(512, (int(nbytes) + 255) // 256 * 256)

@@ -46,6 +46,11 @@ inline int check_table(const octo_page_table* t, int page_size) {
   return OCTO_OK;
 }
 
+// The paged calls' scratch starts behind what octo_decode_attn keeps at the
+// front of a workspace from one call to the next: a status word, and at byte
+// 256 an arrival counter per cache head, at most 65535.
+constexpr size_t kDecodeFront = 256 + 4 * 65536;
+
 // ---- device: the table ------------------------------------------------------
 struct Table {
   const int32_t* pages;

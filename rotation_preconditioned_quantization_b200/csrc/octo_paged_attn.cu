@@ -1250,7 +1250,7 @@ extern "C" size_t octo_paged_attn_workspace(const octo_layout* L, int64_t n_rows
   if (check_layout(L) != OCTO_OK || L->d > 128 || n_rows < 0 || n_seqs < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0)
     return 0;
   // two partial slots and the row copies of each CTA, whatever the sizes
-  return attn_ctas() * (3 * 256 * L->d * sizeof(float) + 2 * 256 * (sizeof(float2) + sizeof(float)) + sizeof(Shared));
+  return kDecodeFront + attn_ctas() * (3 * 256 * L->d * sizeof(float) + 2 * 256 * (sizeof(float2) + sizeof(float)) + sizeof(Shared));
 }
 
 extern "C" int octo_paged_attn(const octo_layout* L, const octo_tables* tab, const octo_pages* pages,
@@ -1301,7 +1301,7 @@ extern "C" int octo_paged_attn(const octo_layout* L, const octo_tables* tab, con
   a.out_bf16 = out_dtype == OCTO_BF16;
   a.lse = lse;
   const int ctas = attn_ctas();
-  a.part_o = static_cast<float4*>(workspace);
+  a.part_o = reinterpret_cast<float4*>(static_cast<unsigned char*>(workspace) + kDecodeFront);
   a.copies = a.part_o + static_cast<size_t>(2) * ctas * (L->d / 4) * 256;
   a.part_ml = reinterpret_cast<float2*>(a.copies + static_cast<size_t>(ctas) * (L->d / 4) * 256);
   a.part_e = reinterpret_cast<float*>(a.part_ml + static_cast<size_t>(2) * ctas * 256);

@@ -650,7 +650,7 @@ extern "C" size_t octo_paged_mass_workspace(const octo_layout* L, int64_t n_rows
   if (check_layout(L) != OCTO_OK || L->d > 128 || n_rows < 0 || n_seqs < 0 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0)
     return 0;
   const size_t tiles = static_cast<size_t>(most_tiles(n_rows, n_seqs, Hq / Hkv)) * Hkv;
-  return 256 + tiles * (static_cast<size_t>(2) * kQRows * L->d * 2 + kQRows * sizeof(float4));
+  return kDecodeFront + tiles * (static_cast<size_t>(2) * kQRows * L->d * 2 + kQRows * sizeof(float4));
 }
 
 extern "C" int octo_paged_mass(const octo_layout* L, const octo_tables* tab, const octo_pages* pages,
@@ -703,7 +703,7 @@ extern "C" int octo_paged_mass(const octo_layout* L, const octo_tables* tab, con
   a.mass_stride = mass_stride;
   a.n_tiles = most_tiles(n_rows, table->n_seqs, g);
   const size_t tiles = static_cast<size_t>(a.n_tiles) * pages->n_heads;
-  a.tiles = static_cast<unsigned char*>(workspace);
+  a.tiles = static_cast<unsigned char*>(workspace) + kDecodeFront;
   a.rows = reinterpret_cast<float*>(a.tiles + tiles * (static_cast<size_t>(2) * kQRows * L->d * 2));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;

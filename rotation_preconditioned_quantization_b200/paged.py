@@ -371,8 +371,8 @@ def paged_attn(layout: api.Layout, tables: api.DeviceTables, q: torch.Tensor, ca
     (``dtype`` float32 or bfloat16, by default q's), and with ``lse`` (True, or a float32 [rows][Hq] tensor) the pair
     (out, lse) with lse = ln sum exp(scale * logits).
 
-    A workspace serves one call at a time: calls that may overlap on the GPU (streams, graphs) need one each. None
-    allocates it for this call.
+    A workspace serves one call at a time, whichever (``decode_attn``'s too): calls that may overlap on the GPU (streams,
+    graphs) need one each. None allocates it for this call.
     """
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype if dtype is None else dtype, device=q.device)

@@ -34,3 +34,12 @@ def test_no_wait_of_the_paged_kernels_is_unbounded():
         assert all("__syncthreads" not in r for r in roles)
     wait = open(os.path.join(src, "octo_paged.cuh")).read().split("bool bar_wait(")[1].split("\n}\n")[0]
     assert re.search(r"it < \(1 << \d+\)", wait) and "while" not in wait
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_paged_scratch_lies_behind_the_words_that_decode_keeps(d):
+    """octo_decode_attn's status word and the arrival counters of its at most 65535 cache heads come first."""
+    lib, lay = _lib.lib(), api.Layout(d, 3)
+    front = 256 + 4 * 65535
+    assert lib.octo_paged_attn_workspace(lay.ref, 1, 1, 1, 1) >= front + 148 * 3 * 256 * d * 4
+    assert lib.octo_paged_mass_workspace(lay.ref, 64, 1, 1, 1) >= front + 64 * d * 4
