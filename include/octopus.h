@@ -434,7 +434,10 @@ OCTO_API int octo_paged_attn(const octo_layout* L, const octo_tables* tables, co
  *   mass_out[i][h][j] = decay * mass_in[i][h][j]
  *                       + sum over the chunk's rows and the head's query heads of exp(logit_j - lse)
  * with the logits, masks and rows of octo_paged_attn and its lse. Slots from
- * seq_lens[i] on are left as they were. The sums have a fixed order.
+ * seq_lens[i] on are left as they were. The sums have a fixed order. A
+ * sequence without new rows gives decay * mass_in, also when the chunk has no
+ * rows at all (n_rows == 0: q, lse and workspace may then be NULL, and with a
+ * NULL mass_out nothing is launched).
  *   mass_in, mass_out device fp32 [n_seqs][n_heads][mass_stride] (the same
  *        array, or not overlapping); mass_in NULL reads as 0. Slots at and
  *        beyond mass_stride are not counted (OCTO_PAGED_BAD_LENGTH).

@@ -673,10 +673,13 @@ extern "C" int octo_paged_mass(const octo_layout* L, const octo_tables* tab, con
   if (!(scale - scale == 0.0f) || !(decay - decay == 0.0f)) return OCTO_EINVAL;  // NaN or infinite
   const int g = Hq / pages->n_heads;
   if (g > 256 || n_rows * g > INT32_MAX - 1024 || pages->n_heads > 65535) return OCTO_EUNSUPPORTED;
-  if (n_rows == 0 || table->n_seqs == 0) return OCTO_OK;
-  if (!q || !lse || !mass_out || !seq_lens || !cu_q) return OCTO_EINVAL;
-  if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return OCTO_EINVAL;
-  if (ws_bytes < octo_paged_mass_workspace(L, n_rows, table->n_seqs, Hq, pages->n_heads)) return OCTO_EWORKSPACE;
+  if (table->n_seqs == 0 || (n_rows == 0 && !mass_out)) return OCTO_OK;
+  if (!mass_out || !seq_lens || !cu_q) return OCTO_EINVAL;
+  if (n_rows > 0) {  // (without rows the masses still decay, and the rest is not read)
+    if (!q || !lse) return OCTO_EINVAL;
+    if (!workspace || reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return OCTO_EINVAL;
+    if (ws_bytes < octo_paged_mass_workspace(L, n_rows, table->n_seqs, Hq, pages->n_heads)) return OCTO_EWORKSPACE;
+  }
   MassArgs a{};
   a.t = make_table(pages, table);
   a.packed = pages->packed;
@@ -703,8 +706,10 @@ extern "C" int octo_paged_mass(const octo_layout* L, const octo_tables* tab, con
   a.mass_stride = mass_stride;
   a.n_tiles = most_tiles(n_rows, table->n_seqs, g);
   const size_t tiles = static_cast<size_t>(a.n_tiles) * pages->n_heads;
-  a.tiles = static_cast<unsigned char*>(workspace) + kDecodeFront;
-  a.rows = reinterpret_cast<float*>(a.tiles + tiles * (static_cast<size_t>(2) * kQRows * L->d * 2));
+  if (n_rows > 0) {
+    a.tiles = static_cast<unsigned char*>(workspace) + kDecodeFront;
+    a.rows = reinterpret_cast<float*>(a.tiles + tiles * (static_cast<size_t>(2) * kQRows * L->d * 2));
+  }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (L->d == 64)

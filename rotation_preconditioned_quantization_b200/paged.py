@@ -414,7 +414,7 @@ def paged_mass(layout: api.Layout, tables: api.DeviceTables, q: torch.Tensor, ls
                workspace: api.Workspace | None = None, stream=None) -> torch.Tensor:
     """Adds the attention weight that each cached token gathers from a chunk: out[i][h][j] = decay * mass[i][h][j] + the
     sum over the chunk's rows and the cache head's query heads of exp(scale * logit_j - lse), for slots j < seq_lens[i];
-    later slots of out are left as they were. q, masks and lse (float32 [rows][Hq]) as in :func:`paged_attn`; mass
+    later slots of out are left as they were. Sequences without new rows, and a chunk without any, decay alone. q, masks and lse (float32 [rows][Hq]) as in :func:`paged_attn`; mass
     float32 [B][heads][slots]; out is mass itself (in place) by default."""
     B, H = seq_lens.numel(), cache.shape[1]
     slots = mass.shape[-1]

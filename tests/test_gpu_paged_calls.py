@@ -50,3 +50,31 @@ def test_one_workspace_serves_decode_and_the_paged_calls_in_turn(cuda_ok):
         assert torch.equal(decode(B, ws), want[B])
         assert ws.status() == 0 and not ws.counters(4 * H).any()
     pool.cache.check()
+
+
+@pytest.mark.parametrize("cu", [None, [0, 0, 0, 0]])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_mass_of_a_chunk_without_rows_decays(cuda_ok, cu, in_place):
+    """A sequence without new rows decays its mass, whether or not another sequence of the batch has some."""
+    pool = pr.Pool(61, 64, 2, 16, 2, [70, 0, 300])
+    m = torch.rand(3, 2, 310, device="cuda", generator=torch.Generator("cuda").manual_seed(2))
+    m0, out = m.clone(), m if in_place else torch.full_like(m, float("nan"))
+    got = paged.paged_mass(pool.lay, pool.tables, torch.empty(0, 4, 64, device="cuda"), torch.empty(0, 4, device="cuda"),
+                           pool.cache, pool.page_table, pool.seq_lens, m, cu_q=None if cu is None else _i32(cu), decay=0.75,
+                           out=out)
+    assert got is out
+    pool.cache.check()
+    for i, n in enumerate(pool.lens):
+        assert torch.equal(out[i, :, :n], 0.75 * m0[i, :, :n])  # one product, rounded once
+        assert torch.equal(out[i, :, n:], m0[i, :, n:]) if in_place else out[i, :, n:].isnan().all()
+
+
+def test_mass_of_a_chunk_without_rows_reports_lengths(cuda_ok):
+    pool = pr.Pool(62, 64, 2, 16, 1, [40], stale=0.0)
+    m = torch.ones(1, 1, 48, device="cuda")
+    call = lambda lens: paged.paged_mass(pool.lay, pool.tables, torch.empty(0, 1, 64, device="cuda"),  # noqa: E731
+                                         torch.empty(0, 1, device="cuda"), pool.cache, pool.page_table, lens, m, decay=0.5)
+    call(_i32([1000]))
+    with pytest.raises(RuntimeError, match="length"):
+        pool.cache.check()
+    assert m.eq(0.5).all()
