@@ -227,10 +227,14 @@ class PagedCache:
 
     def check(self) -> None:
         """Raises if a kernel found a page id outside the pool, a length that the tables do not hold, or gave up a
-        bounded wait (synchronises; clears the word)."""
+        bounded wait (waits for the device's calls, on whatever stream; clears the word)."""
+        if self.status.is_cuda:
+            torch.cuda.synchronize(self.status.device)
         bits = int(self.status.item())
         if bits:
             self.status.zero_()
+            if self.status.is_cuda:  # cleared before a call on another stream can set it again
+                torch.cuda.synchronize(self.status.device)
             names = [n for b, n in ((_lib.PAGED_TIMEOUT, "a wait expired"), (_lib.PAGED_BAD_PAGE, "a page id outside the pool"),
                                     (_lib.PAGED_BAD_LENGTH, "a length or offset that the tables do not hold")) if bits & b]
             raise RuntimeError("paged cache: " + ", ".join(names))

@@ -78,3 +78,22 @@ def test_mass_of_a_chunk_without_rows_reports_lengths(cuda_ok):
     with pytest.raises(RuntimeError, match="length"):
         pool.cache.check()
     assert m.eq(0.5).all()
+
+
+def test_check_waits_for_calls_on_other_streams(cuda_ok):
+    """What a call on another stream than the current one finds is raised, and not lost to the clearing of the word."""
+    pool = pr.Pool(71, 64, 2, 16, 1, [100], stale=0.0)
+    q = _queries(72, 1, 1, 64)
+    table = pool.page_table.clone()
+    table[0, 3] = 1 << 20
+    paged.paged_attn(pool.lay, pool.tables, q, pool.cache, pool.page_table, pool.seq_lens)
+    pool.cache.check()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(40_000_000)  # some twenty milliseconds
+    paged.paged_attn(pool.lay, pool.tables, q, pool.cache, table, pool.seq_lens, stream=side)
+    with pytest.raises(RuntimeError, match="page id"):
+        pool.cache.check()
+    torch.cuda.synchronize()
+    assert int(pool.cache.status.item()) == 0
