@@ -22,6 +22,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import inspect
 from dataclasses import dataclass
 
 import numpy as np
@@ -52,10 +53,13 @@ def _on(index: int, stream, call):
 
 
 def _on_its_stream(f):
-    """With ``stream``, f runs with it current: what f allocates or fills belongs to the stream that uses it."""
+    """With ``stream``, by keyword or by position, f runs with it current: what f allocates or fills belongs to the stream
+    that uses it."""
+    at = list(inspect.signature(f).parameters).index("stream")
+
     @functools.wraps(f)
     def call(*args, **kw):
-        stream = kw.get("stream")
+        stream = args[at] if len(args) > at else kw.get("stream")
         if stream is None:
             return f(*args, **kw)
         with torch.cuda.stream(stream):

@@ -97,3 +97,19 @@ def test_check_waits_for_calls_on_other_streams(cuda_ok):
         pool.cache.check()
     torch.cuda.synchronize()
     assert int(pool.cache.status.item()) == 0
+
+
+def test_stream_by_position_owns_what_the_call_allocates(cuda_ok):
+    pool = pr.Pool(73, 128, 3, 64, 2, [3000, 64])
+    q = _queries(74, 16, 8, 128)
+    args = (pool.lay, pool.tables, q, pool.cache, pool.page_table, pool.seq_lens)
+    want = paged.paged_attn(*args)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)  # the current stream is busy for some ten milliseconds
+    out = paged.paged_attn(*args, None, True, None, None, None, None, None, side)
+    junk = [torch.full((1 << k,), float("nan"), device="cuda") for k in range(10, 25)]
+    side.synchronize()
+    assert torch.equal(out, want)
+    torch.cuda.synchronize()
+    del junk

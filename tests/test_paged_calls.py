@@ -43,3 +43,47 @@ def test_paged_scratch_lies_behind_the_words_that_decode_keeps(d):
     front = 256 + 4 * 65535
     assert lib.octo_paged_attn_workspace(lay.ref, 1, 1, 1, 1) >= front + 148 * 3 * 256 * d * 4
     assert lib.octo_paged_mass_workspace(lay.ref, 64, 1, 1, 1) >= front + 64 * d * 4
+
+
+def _calls():
+    """Each wrapped call with arguments that the device check refuses, up to `stream` by position and by keyword."""
+    lay, tabs, c = _cpu()
+    q, lens, table = torch.zeros(4, 4, 64), _i32([5, 6]), _i32([[0, 1], [2, 3]])
+    m, lse = torch.zeros(2, 2, 32), torch.zeros(4, 4)
+    V = torch.zeros(6, 2, 64, dtype=torch.bfloat16)
+    return {
+        "rope": (paged.rope, [q, torch.zeros(1, 4, dtype=torch.int32), paged.RopeTable((16,), device="cpu")], [None, False, False, None, None]),
+        "paged_append": (paged.paged_append, [lay, tabs, torch.zeros(6, 2, 64), V, c, table, lens, _i32([0, 3, 6])], [None]),
+        "paged_attn": (paged.paged_attn, [lay, tabs, q, c, table, lens], [None, True, None, None, None, None, None]),
+        "paged_mass": (paged.paged_mass, [lay, tabs, q, lse, c, table, lens, m], [None, True, None, 1.0, None, None]),
+        "paged_evict": (paged.paged_evict, [lay, c, table, lens, m, 16, table], [0, 0, None, None, None, None]),
+    }
+
+
+@pytest.mark.parametrize("name", ["rope", "paged_append", "paged_attn", "paged_mass", "paged_evict"])
+def test_stream_is_current_within_the_call_however_it_is_passed(name, monkeypatch):
+    class Entered(Exception):
+        pass
+
+    class Stream:
+        def __init__(self, s):
+            self.s = s
+
+        def __enter__(self):
+            raise Entered(self.s)
+
+        def __exit__(self, *a):
+            return False
+
+    monkeypatch.setattr(torch.cuda, "stream", Stream)
+    f, args, rest = _calls()[name]
+    side = object()
+    with pytest.raises(Entered) as e:
+        f(*args, stream=side)
+    assert e.value.args[0] is side
+    with pytest.raises(Entered) as e:
+        f(*args, *rest, side)
+    assert e.value.args[0] is side
+    for a, kw in ((args, {}), (args, {"stream": None}), (args + rest + [None], {})):
+        with pytest.raises(ValueError, match="CUDA"):
+            f(*a, **kw)
