@@ -401,8 +401,8 @@ extern "C" int octo_paged_write(const octo_layout* L, const octo_pages* pages, c
   if (n_rows < 0 || staged_cap < n_rows || v_row_stride < 0 || v_head_stride < 0) return OCTO_EINVAL;
   if (n_rows > INT32_MAX) return OCTO_EUNSUPPORTED;
   if (pages->n_heads > 65535) return OCTO_EUNSUPPORTED;  // grid.y limit
-  if ((V == nullptr) != (pages->V == nullptr)) return OCTO_EINVAL;
   if (n_rows == 0 || table->n_seqs == 0) return OCTO_OK;
+  if ((V == nullptr) != (pages->V == nullptr)) return OCTO_EINVAL;
   if (!packed || !gamma || !starts || !cu) return OCTO_EINVAL;
   if (reinterpret_cast<uintptr_t>(V) % 16 != 0 || (V && (v_row_stride % 8 != 0 || v_head_stride % 8 != 0)))
     return OCTO_EINVAL;

@@ -113,3 +113,17 @@ def test_stream_by_position_owns_what_the_call_allocates(cuda_ok):
     assert torch.equal(out, want)
     torch.cuda.synchronize()
     del junk
+
+
+def test_no_tokens_into_a_pool_with_values(cuda_ok):
+    lay = api.Layout(64, 2)
+    tabs = api.DeviceTables.build(lay, 0, 2)
+    cache = paged.PagedCache.empty(lay, 2, 2, 16)
+    before = [x.clone() for x in (cache.packed, cache.gamma, cache.V)]
+    V = torch.empty(0, 2, 64, dtype=torch.bfloat16, device="cuda")
+    paged.paged_write(lay, api.Cache.empty(lay, 2, 8), V, cache, _i32([[1]]), _i32([3]), _i32([0, 0]))
+    for dt in (torch.bfloat16, torch.float32):
+        paged.paged_append(lay, tabs, torch.empty(0, 2, 64, dtype=dt, device="cuda"), V, cache, _i32([[1]]), _i32([3]),
+                           _i32([0, 0]))
+    cache.check()
+    assert all(torch.equal(a, b) for a, b in zip(before, (cache.packed, cache.gamma, cache.V)))

@@ -87,3 +87,12 @@ def test_stream_is_current_within_the_call_however_it_is_passed(name, monkeypatc
     for a, kw in ((args, {}), (args, {"stream": None}), (args + rest + [None], {})):
         with pytest.raises(ValueError, match="CUDA"):
             f(*a, **kw)
+
+
+def test_writing_no_rows_needs_no_addresses():
+    """torch gives an empty tensor the address 0: with no rows, V says nothing about the pool's values."""
+    lay = api.Layout(64, 2)
+    pages, table = _lib.OctoPages(256, 256, 256, 4, 2, 16, None), _lib.OctoPageTable(256, 4, 2, 4)
+    f = _lib.lib().octo_paged_write
+    assert f(lay.ref, ctypes.byref(pages), ctypes.byref(table), 256, 256, 8, None, 128, 64, 0, 256, 256, None) == OK
+    assert f(lay.ref, ctypes.byref(pages), ctypes.byref(table), 256, 256, 8, None, 128, 64, 4, 256, 256, None) == EINVAL
