@@ -92,15 +92,21 @@ class RopeTable:
     scale theta^(-i / F) runs over all F = sum(sections) of them, or one per axis, theta^(-j / sections[k])."""
 
     def __init__(self, sections, theta: float = 10000.0, per_axis: bool = False, device="cuda"):
-        self.sections = tuple(int(s) for s in sections)
-        sec = np.asarray(self.sections, np.int32)
+        self._sections = tuple(int(s) for s in sections)
+        sec = np.asarray(self._sections, np.int32)
         f = np.zeros(max(1, int(sum(self.sections))), np.uint64)
         _lib.check(_lib.lib().octo_rope_freqs(float(theta), len(sec), sec.ctypes.data, int(bool(per_axis)), f.ctypes.data),
                    "octo_rope_freqs")
-        self.theta, self.per_axis = float(theta), bool(per_axis)
+        self._theta, self._per_axis = float(theta), bool(per_axis)
         self.c_sections = sec
         self.freqs = torch.from_numpy(f.view(np.int64)).to(device)
-        self.sections_ptr, self.freqs_ptr = sec.ctypes.data, self.freqs.data_ptr()
+        self.sections_ptr = sec.ctypes.data
+
+    # of the frequencies as computed: not to be assigned
+    sections = property(lambda self: self._sections)
+    theta = property(lambda self: self._theta)
+    per_axis = property(lambda self: self._per_axis)
+    freqs_ptr = property(lambda self: self.freqs.data_ptr())
 
 
 def _end(t: torch.Tensor) -> int:
@@ -141,7 +147,10 @@ def rope(q: torch.Tensor, positions: torch.Tensor, table: RopeTable, k: torch.Te
     if dt is None or q.dim() != 3:
         raise ValueError(f"q must be float32 or bfloat16 [tokens][heads][d], got {q.dtype} {tuple(q.shape)}")
     n, _, d = q.shape
-    axes = len(table.sections)
+    axes, freqs = len(table.sections), table.freqs
+    if freqs.dtype is not torch.int64 or freqs.numel() < sum(table.sections) or not freqs.is_contiguous():
+        raise ValueError(f"the table's freqs must be contiguous int64 [{sum(table.sections)}], got {freqs.dtype} "
+                         f"{tuple(freqs.shape)}")
     if positions.dtype is not _I32 or positions.shape != (axes, n) or (n > 1 and positions.stride(1) != 1):
         raise ValueError(f"positions must be int32 [{axes}][{n}], contiguous in its last dimension, got "
                          f"{positions.dtype} {tuple(positions.shape)}")
@@ -155,11 +164,11 @@ def rope(q: torch.Tensor, positions: torch.Tensor, table: RopeTable, k: torch.Te
         k_out, c = _rope_pair(k, k_out, "k_out")
         b = _byref(c)
     index = q.get_device()
-    _same_device(index, k, positions, table.freqs, out, k_out)
+    _same_device(index, k, positions, freqs, out, k_out)
     stride = positions.stride(0)
     st = _on(index, stream, lambda s: _lib.lib().octo_rope(
         _byref(a), b, dt, n, d, positions.data_ptr(), stride if stride > n else n, axes, table.sections_ptr,
-        table.freqs_ptr, interleaved, inverse, s))
+        freqs.data_ptr(), interleaved, inverse, s))
     if st:
         _lib.check(st, "octo_rope")
     return out if k is None else (out, k_out)
@@ -194,9 +203,27 @@ class PagedCache:
             raise ValueError("the cache's tensors must be on one device")
         self.shape = (n, h, p.shape[2], s, None if v is None else v.shape[3])  # pages, heads, words, page size, d
         self.index = p.get_device()
-        self.c = _lib.OctoPages(p.data_ptr(), g.data_ptr(), None if v is None else v.data_ptr(), n, h, s,
-                                self.status.data_ptr())
-        self.ref = _byref(self.c)
+        self._held = (p, g, v, self.status)
+        self._at = (p.data_ptr(), g.data_ptr(), None if v is None else v.data_ptr(), self.status.data_ptr())
+        self._ref = _byref(_lib.OctoPages(*self._at[:3], n, h, s, self._at[3]))
+
+    def current(self) -> PagedCache:
+        """The pool, described anew (and checked) if a field was assigned or a tensor's memory moved since: calls use the
+        tensors that it holds now."""
+        p, g, v, s = self._held
+        if (p is not self.packed or g is not self.gamma or v is not self.V or s is not self.status or
+                self._at != (p.data_ptr(), g.data_ptr(), None if v is None else v.data_ptr(), s.data_ptr())):
+            self.__post_init__()
+        return self
+
+    @property
+    def ref(self):
+        """The ``octo_pages`` of the tensors held now, for the C ABI."""
+        return self.current()._ref
+
+    @property
+    def c(self) -> _lib.OctoPages:
+        return self.ref._obj
 
     @classmethod
     def empty(cls, layout: api.Layout, n_pages: int, n_heads: int, page_size: int, values: bool = True, device="cuda"):
@@ -245,7 +272,9 @@ class PagedCache:
 
 
 def _check_pool(layout: api.Layout, cache: PagedCache, values: bool):
+    """The pool fits the layout. Comes before any other look at the pool's shape."""
     c = layout.c
+    cache.current()
     if cache.shape[2] != c.words:
         raise ValueError(f"the cache holds {cache.shape[2]} words per key, {layout!r} has {c.words}")
     if cache.shape[4] is None:
@@ -298,7 +327,7 @@ def paged_write(layout: api.Layout, staged: api.Cache, V: torch.Tensor | None, c
     index = cache.index
     _same_device(index, p, g, V, page_table, starts, cu)
     st = _on(index, stream, lambda s: _lib.lib().octo_paged_write(
-        layout.ref, cache.ref, _byref(t), p.data_ptr(), g.data_ptr(), cap, pv, sr, sh, rows, starts.data_ptr(),
+        layout.ref, cache._ref, _byref(t), p.data_ptr(), g.data_ptr(), cap, pv, sr, sh, rows, starts.data_ptr(),
         cu.data_ptr(), s))
     if st:
         _lib.check(st, "octo_paged_write")
@@ -405,7 +434,7 @@ def paged_attn(layout: api.Layout, tables: api.DeviceTables, q: torch.Tensor, ca
     def call(s):
         ws = _scratch(workspace, lib.octo_paged_attn_workspace(layout.ref, rows, B, Hq, cache.shape[1]), cache)
         return lib.octo_paged_attn(
-            layout.ref, tables.ref, cache.ref, _byref(t), seq_lens.data_ptr(), q.data_ptr(), dt, q.stride(0), q.stride(1),
+            layout.ref, tables.ref, cache._ref, _byref(t), seq_lens.data_ptr(), q.data_ptr(), dt, q.stride(0), q.stride(1),
             rows, Hq, cu_q.data_ptr(), causal, layout.c.d ** -0.5 if scale is None else scale, out.data_ptr(), odt,
             None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel() * 4, s)
 
@@ -424,6 +453,7 @@ def paged_mass(layout: api.Layout, tables: api.DeviceTables, q: torch.Tensor, ls
     sum over the chunk's rows and the cache head's query heads of exp(scale * logit_j - lse), for slots j < seq_lens[i];
     later slots of out are left as they were. Sequences without new rows, and a chunk without any, decay alone. q, masks and lse (float32 [rows][Hq]) as in :func:`paged_attn`; mass
     float32 [B][heads][slots]; out is mass itself (in place) by default."""
+    _check_pool(layout, cache, False)
     B, H = seq_lens.numel(), cache.shape[1]
     slots = mass.shape[-1]
     _dense(mass, "mass", _F32, (B, H, slots))
@@ -434,7 +464,6 @@ def paged_mass(layout: api.Layout, tables: api.DeviceTables, q: torch.Tensor, ls
         if out.data_ptr() != mass.data_ptr() and abs(out.data_ptr() - mass.data_ptr()) < 4 * mass.numel():
             raise ValueError("out must be mass itself or not overlap it")
     _dense(lse, "lse", _F32, q.shape[:2])
-    _check_pool(layout, cache, False)
     dt, rows, Hq, B, cu_q, t = _chunk(layout, tables, q, cache, page_table, seq_lens, cu_q)
     index, lib = cache.index, _lib.lib()
     _same_device(index, lse, mass, out)
@@ -442,7 +471,7 @@ def paged_mass(layout: api.Layout, tables: api.DeviceTables, q: torch.Tensor, ls
     def call(s):
         ws = _scratch(workspace, lib.octo_paged_mass_workspace(layout.ref, rows, B, Hq, H), cache)
         return lib.octo_paged_mass(
-            layout.ref, tables.ref, cache.ref, _byref(t), seq_lens.data_ptr(), q.data_ptr(), dt, q.stride(0), q.stride(1),
+            layout.ref, tables.ref, cache._ref, _byref(t), seq_lens.data_ptr(), q.data_ptr(), dt, q.stride(0), q.stride(1),
             rows, Hq, cu_q.data_ptr(), causal, layout.c.d ** -0.5 if scale is None else scale, lse.data_ptr(), decay,
             mass.data_ptr(), out.data_ptr(), slots, ws.data_ptr(), ws.numel() * 4, s)
 
@@ -493,7 +522,7 @@ def paged_evict(layout: api.Layout, cache: PagedCache, page_table: torch.Tensor,
     t, z = _table(page_table, B), _table(dst_table, B, "dst_table")
     _same_device(index, page_table, seq_lens, mass, dst_table, dst.packed, kept, new_lens, new_mass)
     st = _on(index, stream, lambda s: _lib.lib().octo_paged_evict(
-        layout.ref, cache.ref, _byref(t), seq_lens.data_ptr(), mass.data_ptr(), slots, keep, sink, recent, dst.ref,
+        layout.ref, cache._ref, _byref(t), seq_lens.data_ptr(), mass.data_ptr(), slots, keep, sink, recent, dst._ref,
         _byref(z), kept.data_ptr(), new_lens.data_ptr(), new_mass.data_ptr(), s))
     if st:
         _lib.check(st, "octo_paged_evict")

@@ -127,3 +127,26 @@ def test_no_tokens_into_a_pool_with_values(cuda_ok):
                            _i32([0, 0]))
     cache.check()
     assert all(torch.equal(a, b) for a, b in zip(before, (cache.packed, cache.gamma, cache.V)))
+
+
+def test_a_pool_whose_tensors_are_replaced(cuda_ok):
+    """A call uses the tensors that the pool holds then, as api.Cache's calls do: also more pages than before."""
+    a, b = pr.Pool(81, 64, 2, 16, 2, [100]), pr.Pool(82, 64, 2, 16, 2, [400])
+    b.tables = a.tables
+    q = _queries(83, 5, 4, 64)
+    call = lambda cache: paged.paged_attn(b.lay, b.tables, q, cache, b.page_table, b.seq_lens)  # noqa: E731
+    want = call(b.cache)
+    old = (a.cache.packed, a.cache.gamma, a.cache.V)  # (kept: the old addresses stay valid)
+    a.cache.packed, a.cache.gamma, a.cache.V = b.cache.packed, b.cache.gamma, b.cache.V
+    assert torch.equal(call(a.cache), want)
+    a.cache.check()
+    a.cache.V = torch.zeros_like(b.cache.V)
+    assert not call(a.cache).any()
+    assert old[0].shape[0] < b.cache.n_pages == a.cache.n_pages
+
+
+def test_rope_frequencies_that_are_replaced(cuda_ok):
+    q, pos = torch.randn(5, 2, 64, device="cuda"), torch.arange(5, dtype=torch.int32, device="cuda")[None] * 1000
+    a, b = paged.RopeTable((32,), 10000.0), paged.RopeTable((32,), 500.0)
+    old, a.freqs = a.freqs, b.freqs.clone()
+    assert torch.equal(paged.rope(q, pos, a), paged.rope(q, pos, b)) and old.shape == b.freqs.shape

@@ -96,3 +96,20 @@ def test_writing_no_rows_needs_no_addresses():
     f = _lib.lib().octo_paged_write
     assert f(lay.ref, ctypes.byref(pages), ctypes.byref(table), 256, 256, 8, None, 128, 64, 0, 256, 256, None) == OK
     assert f(lay.ref, ctypes.byref(pages), ctypes.byref(table), 256, 256, 8, None, 128, 64, 4, 256, 256, None) == EINVAL
+
+
+def test_a_pool_describes_the_tensors_that_it_holds_now():
+    lay, tabs, c = _cpu(pages=4)
+    big = paged.PagedCache.empty(lay, 9, 2, 32, device="cpu")
+    c.packed, c.gamma, c.V = big.packed, big.gamma, big.V
+    now = c.ref._obj
+    assert (now.packed, now.gamma, now.V, now.n_pages, now.page_size) == (big.packed.data_ptr(), big.gamma.data_ptr(),
+                                                                          big.V.data_ptr(), 9, 32)
+    assert (c.n_pages, c.n_heads, c.page_size) == (9, 2, 32)
+    c.V = None
+    assert c.ref._obj.V is None
+    c.status = torch.zeros(1, dtype=torch.int32)
+    assert c.ref._obj.status == c.status.data_ptr()
+    c.gamma = c.gamma[:3]  # no pool's: refused where it is used
+    with pytest.raises(ValueError, match="gamma"):
+        paged.paged_attn(lay, tabs, torch.zeros(2, 2, 64), c, _i32([[0], [1]]), _i32([5, 6]))
