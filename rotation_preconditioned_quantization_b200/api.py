@@ -111,6 +111,15 @@ class DeviceTables:
     def ref(self):
         return ctypes.byref(self.c)
 
+    def check(self, layout: Layout):
+        """Refuses tables of another layout: the kernels read as many entries as the layout has."""
+        c, s = layout.c, self.signs.shape
+        if self.dir_c.numel() != c.n_dir or self.rho_c.numel() != c.n_rho or len(s) != 2 or s[0] < 1 or s[1] != c.d:
+            raise ValueError(f"the tables hold {self.dir_c.numel()} directions, {self.rho_c.numel()} norms and signs "
+                             f"{tuple(s)}: they are not of {layout!r}")
+        if c.qjl and self.qjl_S is not None and self.qjl_S.shape != (s[0], c.d, c.d):
+            raise ValueError(f"the tables' qjl_S must be {(s[0], c.d, c.d)}, got {tuple(self.qjl_S.shape)}")
+
 
 @dataclass
 class Cache:
@@ -167,6 +176,7 @@ def _check_cache(layout: Layout, tables: DeviceTables, cache: Cache, heads: int,
                              f"and [{H}][{cap}] float32")
     if heads > H:
         raise ValueError(f"{heads} heads requested, the cache holds {H}")
+    tables.check(layout)
     dev = cache.gamma.device
     for t in (cache.packed, cache.qjl_bits, cache.qjl_norm, tables.dir_c, tables.rho_c, tables.signs,
               tables.qjl_S) + others:
@@ -193,6 +203,8 @@ def encode(layout: Layout, tables: DeviceTables, keys: torch.Tensor, cache: Cach
     off = cache.length if token_offset is None else int(token_offset)
     n_heads, n_tok = int(keys.shape[0]), int(keys.shape[1])
     _check_cache(layout, tables, cache, n_heads, keys)
+    if tables.dir_t.numel() < layout.n_dir - 1 or tables.rho_t.numel() < layout.n_rho - 1:
+        raise ValueError(f"the tables hold {tables.dir_t.numel()} and {tables.rho_t.numel()} thresholds: they are not of {layout!r}")
     st = _lib.lib().octo_encode(layout.ref, tables.ref, _ptr(keys), dt, n_heads, n_tok, keys.stride(0), keys.stride(1),
                                 cache.cap, off, _ptr(cache.packed), _ptr(cache.gamma), _ptr(cache.qjl_bits),
                                 _ptr(cache.qjl_norm), _stream_ptr(stream))

@@ -372,6 +372,7 @@ def _chunk(layout, tables, q, cache, page_table, seq_lens, cu_q):
         cu_q = torch.arange(B + 1, dtype=_I32, device=q.device) * (rows // B)
     _vector(cu_q, "cu_q", B + 1)
     t = _table(page_table, B)
+    tables.check(layout)
     _same_device(cache.index, q, page_table, seq_lens, cu_q, tables.dir_c, tables.signs)
     return dt, rows, Hq, B, cu_q, t
 

@@ -113,3 +113,36 @@ def test_a_pool_describes_the_tensors_that_it_holds_now():
     c.gamma = c.gamma[:3]  # no pool's: refused where it is used
     with pytest.raises(ValueError, match="gamma"):
         paged.paged_attn(lay, tabs, torch.zeros(2, 2, 64), c, _i32([[0], [1]]), _i32([5, 6]))
+
+
+@pytest.mark.parametrize("d,b", [(128, 2), (64, 3), (64, 4)])
+def test_tables_of_another_layout_are_refused(d, b):
+    """Codebooks and sign rows of another d or b would be read past their end."""
+    lay, own, c = _cpu()
+    tabs = api.DeviceTables.build(api.Layout(d, b), 0, 2, device="cpu")
+    q, lens, table, V = torch.zeros(4, 4, 64), _i32([5, 6]), _i32([[0, 1], [2, 3]]), torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    flat = api.Cache.empty(lay, 2, 16, device="cpu")
+    for t, match in ((tabs, "tables"), (own, "CUDA")):
+        with pytest.raises(ValueError, match=match):
+            paged.paged_attn(lay, t, q, c, table, lens)
+        with pytest.raises(ValueError, match=match):
+            paged.paged_mass(lay, t, q, torch.zeros(4, 4), c, table, lens, torch.zeros(2, 2, 32))
+    for f in (lambda: api.encode(lay, tabs, torch.zeros(2, 4, 64), flat),
+              lambda: api.dequant(lay, tabs, flat, 4),
+              lambda: api.decode_attn(lay, tabs, torch.zeros(1, 4, 1, 64), flat, None, 2, kv_len=4, logits=True)):
+        with pytest.raises(ValueError, match="tables"):
+            f()
+
+
+def test_sketch_matrices_of_other_heads_are_refused():
+    lay = api.Layout(64, 3, qjl=True)
+    tabs = api.DeviceTables.build(lay, 0, 4, device="cpu")
+    tabs.qjl_S = tabs.qjl_S[:2]
+    with pytest.raises(ValueError, match="tables"):
+        api.encode(lay, tabs, torch.zeros(4, 4, 64), api.Cache.empty(lay, 4, 16, device="cpu"))
+    lay = api.Layout(64, 3)
+    for k in ("dir_t", "rho_t"):
+        tabs = api.DeviceTables.build(lay, 0, 4, device="cpu")
+        setattr(tabs, k, getattr(tabs, k)[:2])
+        with pytest.raises(ValueError, match="tables"):
+            api.encode(lay, tabs, torch.zeros(4, 4, 64), api.Cache.empty(lay, 4, 16, device="cpu"))
