@@ -417,7 +417,8 @@ OCTO_API int octo_paged_write(const octo_layout* L, const octo_pages* pages, con
  * of two per row), weights and V as bf16; sums and softmax statistics are
  * fp32 (out is divided by the sum of the rounded weights, lse is that of the
  * unrounded ones). Values of slots that a row does not see, but another row of its
- * sequence does, must be finite. Two launches.
+ * sequence does, must be finite, and the magnitudes of a sequence's values sum
+ * to less than 2^60 per coordinate. Two launches.
  * Supported: d in {64, 128}, b in {2, 3, 4}, Hq / n_heads <= 256.
  * Errors: OCTO_EINVAL, OCTO_EUNSUPPORTED, OCTO_EWORKSPACE. n_rows == 0
  * launches nothing. */

@@ -614,7 +614,11 @@ __device__ __forceinline__ float max3_abs(float a, float b, float c) {
 // A row's running state, and the tensor-memory columns of its S (then P) and
 // O. Weights are 2^(logit - ref) for a reference that needs only be near
 // (bf16 and fp32 keep their precision whatever the exponent): it is set by a
-// row's first slots and raised when a logit might pass it by 100.
+// row's first slots and raised when a logit might pass it by kAsk. So weights
+// stay below 2^kAsk, and their products with values finite where a row's
+// values sum to less than 2^60 in magnitude. (A smaller kAsk asks for looks at
+// the logits that a wide spread of norms does not warrant.)
+constexpr float kAsk = 64.0f;
 template <int D, bool LSE>  // LSE: lse is asked for
 struct Row {
   uint32_t S, O;
@@ -748,7 +752,7 @@ struct Row {
       }
     }
     // (a NaN among them, or an infinite norm, fails the comparison)
-    const bool ask = there && !(fmaxf(top[0], top[1]) * gmax <= ref + 100.0f);
+    const bool ask = there && !(fmaxf(top[0], top[1]) * gmax <= ref + kAsk);
     if (__any_sync(0xffffffffu, ask)) {
       float high = -INFINITY;
       float2 y[16];

@@ -405,7 +405,7 @@ def paged_attn(layout: api.Layout, tables: api.DeviceTables, q: torch.Tensor, ca
     q [rows][Hq][d] (float32 or bfloat16): rows cu_q[i] .. cu_q[i+1] - 1 (cu_q int32 [B + 1]; None: the same number for
     each) are the last tokens of sequence i, whose cache holds seq_lens[i] slots. With ``causal`` each new token sees the
     slots up to its own, else all of its sequence. A row that sees nothing gives 0 (lse -inf). Values of slots that one row
-    of a sequence sees must be finite for its other rows too. Returns out [rows][Hq][d]
+    of a sequence sees must be finite for its other rows too, and sum to less than 2^60 in magnitude. Returns out [rows][Hq][d]
     (``dtype`` float32 or bfloat16, by default q's), and with ``lse`` (True, or a float32 [rows][Hq] tensor) the pair
     (out, lse) with lse = ln sum exp(scale * logits).
 

@@ -150,3 +150,32 @@ def test_rope_frequencies_that_are_replaced(cuda_ok):
     a, b = paged.RopeTable((32,), 10000.0), paged.RopeTable((32,), 500.0)
     old, a.freqs = a.freqs, b.freqs.clone()
     assert torch.equal(paged.rope(q, pos, a), paged.rope(q, pos, b)) and old.shape == b.freqs.shape
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_large_values_behind_a_rise_of_the_logits(cuda_ok, d):
+    """Whole key tiles whose logits pass the first tile's by far (2^87 in the weights by the first tile's reference),
+    with values of 2^36: a row's output is as exact as bf16 weights say, and lies between the values that it averages.
+    Enough equal rows that a CTA walks from an item's first tile into its next ones."""
+    rows, n = 256 * 60, 1024
+    pool = pr.Pool(91 + d, d, 3, 64, 1, [n])
+    rng = np.random.default_rng(5)
+    pool.words[:] = pool.words[:1, :, :, :1]  # one direction throughout
+    p, o = pool.slots(0)
+    pool.V[p, 0, o] = inputs.to_bf16((2.0 ** 36 * rng.uniform(1.0, 2.0, (n, d))).astype(np.float32))
+    pool.gamma[p, 0, o] = np.where(np.arange(n) < 128, 0.01, 1.0).astype(np.float32)
+    _, u, _ = pool.keys(0, 0)
+    R = pr.codec.rotation_matrix(pool.signs[0])
+    want = 88.0 * np.log(2.0)  # the logit of a slot behind the first tile
+    q = (u[0] @ R / (u[0] @ u[0]) * want * np.sqrt(d))[None, None].astype(np.float32)
+    pool.to("cuda")
+    out, lse = paged.paged_attn(pool.lay, pool.tables, torch.from_numpy(q).cuda().expand(rows, 1, d), pool.cache,
+                                pool.page_table, pool.seq_lens, causal=False, lse=True)
+    pool.cache.check()
+    ref, rl, mag, dmax = pr.attn(pool, q, [0, 1], False)
+    assert abs(rl[0, 0] - want - np.log(n - 128.0)) < 1e-3 and dmax.max() < 0.5
+    ref, mag, dmax = (np.broadcast_to(x, (rows,) + x.shape[1:]) for x in (ref, mag, dmax))
+    pr.check_attn(out, ref, mag, dmax, False)
+    assert np.all(np.abs(lse.cpu().numpy() - rl[0, 0]) <= dmax + 2.0 ** -20 * (1 + abs(rl[0, 0])))
+    v, got = pool.V[p, 0, o], out.cpu().numpy()
+    assert np.all(got >= v.min(0) * (1 - 2.0 ** -7)) and np.all(got <= v.max(0) * (1 + 2.0 ** -7))
