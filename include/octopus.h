@@ -387,7 +387,9 @@ OCTO_API int octo_rope_freqs(double theta, int n_axes, const int32_t* sections, 
  *                  h*v_head_stride (elements), d contiguous; pointer and
  *                  strides multiples of 16 bytes. The pool's V may be NULL
  *                  with V NULL (keys only).
- *   starts, cu     device int32 [n_seqs], [n_seqs + 1].
+ *   starts, cu     device int32 [n_seqs], [n_seqs + 1]. Rows from cu[n_seqs]
+ *                  on (a batch padded to a fixed size) are left alone, as in
+ *                  the chunk calls; others without a place are reported.
  * Two tokens must not go to one slot. Errors: OCTO_EINVAL, and
  * OCTO_EUNSUPPORTED for a layout outside the paged set. n_rows == 0 launches
  * nothing. */

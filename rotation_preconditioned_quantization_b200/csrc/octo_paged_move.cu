@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(256) paged_write_kernel(const __grid_constant_
       const int pg = page_of(a.t, lo, static_cast<int>(slot));
       page = static_cast<int64_t>(pg) * a.t.n_heads + h;
       if (pg >= 0) to = page * a.t.page_size + page_offset(a.t, static_cast<int>(slot));
-    } else {
+    } else if (r < __ldg(a.cu + a.t.n_seqs)) {  // (rows behind the last sequence are none of its tokens)
       report(a.t.status, OCTO_PAGED_BAD_LENGTH);
     }
     s_dst[t] = to;

@@ -302,7 +302,8 @@ def paged_write(layout: api.Layout, staged: api.Cache, V: torch.Tensor | None, c
 
     staged: a contiguous :class:`api.Cache` whose ``cache.n_heads`` heads hold the rows' codes from token 0 (``encode``
     of the packed keys); V [rows][heads][d] bfloat16, any row and head strides that are multiples of 8 elements, or None
-    for a cache without values; starts int32 [B], cu int32 [B + 1]. No two tokens may go to one slot.
+    for a cache without values; starts int32 [B], cu int32 [B + 1]. No two tokens may go to one slot. Rows
+    from cu[B] on (a batch padded to a fixed size) are left alone.
     """
     _check_pool(layout, cache, False)
     B, H, W, d = starts.numel(), cache.shape[1], cache.shape[2], layout.c.d

@@ -179,3 +179,25 @@ def test_large_values_behind_a_rise_of_the_logits(cuda_ok, d):
     assert np.all(np.abs(lse.cpu().numpy() - rl[0, 0]) <= dmax + 2.0 ** -20 * (1 + abs(rl[0, 0])))
     v, got = pool.V[p, 0, o], out.cpu().numpy()
     assert np.all(got >= v.min(0) * (1 - 2.0 ** -7)) and np.all(got <= v.max(0) * (1 + 2.0 ** -7))
+
+
+def test_write_leaves_the_rows_behind_the_last_sequence(cuda_ok):
+    """A batch padded to a fixed number of rows, as a captured call has it: the rows behind the last sequence are no
+    tokens (the chunk calls leave theirs alone too). Those before the first sequence's are still reported."""
+    lay = api.Layout(64, 2)
+    cache = paged.PagedCache.empty(lay, 3, 1, 16)
+    staged = api.Cache.empty(lay, 1, 40)
+    staged.gamma.fill_(3.0)
+    V = torch.ones(40, 1, 64, dtype=torch.bfloat16, device="cuda")
+    for cu in ([0, 4, 7], [0, 7, 7], [0, 0, 7]):
+        cache.gamma.zero_()
+        paged.paged_write(lay, staged, V, cache, _i32([[0], [2]]), _i32([1, 2]), _i32(cu))
+        cache.check()
+        assert cache.gamma[0, 0, 1:1 + cu[1]].eq(3).all() and cache.gamma[2, 0, 2:2 + 7 - cu[1]].eq(3).all()
+        assert cache.gamma.sum() == 21
+    paged.paged_write(lay, staged, V, cache, _i32([[0], [2]]), _i32([1, 2]), _i32([0, 0, 0]))
+    cache.check()
+    assert cache.gamma.sum() == 21
+    paged.paged_write(lay, staged, V, cache, _i32([[0], [2]]), _i32([1, 2]), _i32([1, 4, 7]))
+    with pytest.raises(RuntimeError, match="length"):
+        cache.check()
