@@ -355,7 +355,8 @@ enum octo_paged_status {
  * position.
  *   x0, y0  device rows [n_tokens][heads0][d] in and out, dtype OCTO_F32 or
  *           OCTO_BF16, element strides (token, head), the last axis
- *           contiguous; y may be x, and must not overlap it otherwise.
+ *           contiguous; y may be x, and must not overlap it otherwise, nor the
+ *           other pair's tensors.
  *   x1, y1  the second pair of tensors, heads1 heads (0: none).
  *   positions device int32 [n_axes][pos_stride].
  *   freqs   device uint64 [F], from octo_rope_freqs.

@@ -23,6 +23,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import inspect
+import math
 from dataclasses import dataclass
 
 import numpy as np
@@ -113,6 +114,20 @@ def _end(t: torch.Tensor) -> int:
     return t.data_ptr() + t.element_size() * (1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride())))
 
 
+def _meet(x: torch.Tensor, y: torch.Tensor) -> bool:
+    """Whether two [tokens][heads][d] tensors of one type may share memory. Strided views that lie between one another's
+    rows, as those of a fused projection, do not: their rows repeat at a distance at which they stay apart."""
+    if not x.numel() or not y.numel() or x.data_ptr() >= _end(y) or y.data_ptr() >= _end(x):
+        return False
+    gap = (y.data_ptr() - x.data_ptr()) // x.element_size()
+    for dims in (1, 2):  # tokens repeat, with a token's heads as one run; or tokens and heads repeat
+        m = math.gcd(*(t.stride(k) for t in (x, y) for k in range(dims) if t.shape[k] > 1))
+        runs = [t.shape[2] + ((t.shape[1] - 1) * t.stride(1) if dims == 1 else 0) for t in (x, y)]
+        if m and (y.data_ptr() - x.data_ptr()) % x.element_size() == 0 and gap % m >= runs[0] and gap % m + runs[1] <= m:
+            return False
+    return True
+
+
 def _rope_pair(x: torch.Tensor, y: torch.Tensor | None, what: str):
     """(output, octo_rope_tensor) of one of rope's tensors."""
     sx = x.stride()
@@ -125,7 +140,8 @@ def _rope_pair(x: torch.Tensor, y: torch.Tensor | None, what: str):
             raise ValueError(f"{what} must have its input's shape and type")
         if any(s == 0 and n > 1 for n, s in zip(y.shape, sy)):
             raise ValueError(f"{what} must not be an expanded view")
-        if (y.data_ptr() != x.data_ptr() or sx != sy) and x.numel() and y.data_ptr() < _end(x) and x.data_ptr() < _end(y):
+        same = y.data_ptr() == x.data_ptr() and all(n == 1 or a == b for n, a, b in zip(x.shape, sx, sy))
+        if not same and _meet(x, y):
             raise ValueError(f"{what} must be the input itself or not overlap it")
     if (sx[2] != 1 or sy[2] != 1) and x.shape[2] > 1:
         raise ValueError("rope's tensors must be contiguous in their last dimension")
@@ -141,7 +157,8 @@ def rope(q: torch.Tensor, positions: torch.Tensor, table: RopeTable, k: torch.Te
     positions[axis(i)][token] * f_i; coordinates from 2F on are copied. positions is int32 [axes][tokens].
 
     ``inverse`` turns back; as the rotation is orthogonal this is also the gradient: grad_q = rope(grad_out, ...,
-    inverse=True). out / k_out may be the inputs (in place). Returns the rotated q, or (q, k).
+    inverse=True). out / k_out may be their own inputs (in place), and must not overlap anything else of the call.
+    Returns the rotated q, or (q, k).
     """
     dt = _DTYPES.get(q.dtype)
     if dt is None or q.dim() != 3:
@@ -156,12 +173,16 @@ def rope(q: torch.Tensor, positions: torch.Tensor, table: RopeTable, k: torch.Te
                          f"{positions.dtype} {tuple(positions.shape)}")
     if axes > 1 and positions.stride(0) < n:
         raise ValueError("positions must not be an expanded view: its rows overlap")
+    out_given = out is not None
     out, a = _rope_pair(q, out, "out")
     b = None
     if k is not None:
         if k.dtype is not q.dtype or k.dim() != 3 or k.shape[0] != n or k.shape[2] != d:
             raise ValueError(f"k must be {q.dtype} [{n}][heads][{d}], got {k.dtype} {tuple(k.shape)}")
+        given = out_given or k_out is not None
         k_out, c = _rope_pair(k, k_out, "k_out")
+        if given and (_meet(out, k) or _meet(k_out, q) or _meet(out, k_out)):
+            raise ValueError("out and k_out must not overlap one another, nor the other's input")
         b = _byref(c)
     index = q.get_device()
     _same_device(index, k, positions, freqs, out, k_out)

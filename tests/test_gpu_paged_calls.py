@@ -201,3 +201,14 @@ def test_write_leaves_the_rows_behind_the_last_sequence(cuda_ok):
     paged.paged_write(lay, staged, V, cache, _i32([[0], [2]]), _i32([1, 2]), _i32([1, 4, 7]))
     with pytest.raises(RuntimeError, match="length"):
         cache.check()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_rope_into_another_part_of_a_fused_buffer(cuda_ok, dtype):
+    """Outputs between the rows of their own inputs, and of the other tensor's, that meet none of them."""
+    g = torch.Generator("cuda").manual_seed(7)
+    x = torch.randn(33, 10, 64, device="cuda", generator=g).to(dtype)
+    pos, table = torch.arange(33, dtype=torch.int32, device="cuda")[None] * 77, paged.RopeTable((32,))
+    want = paged.rope(x[:, :4].clone(), pos, table, k=x[:, 4:5].clone())
+    paged.rope(x[:, :4], pos, table, k=x[:, 4:5], out=x[:, 5:9], k_out=x[:, 9:])
+    assert torch.equal(x[:, 5:9], want[0]) and torch.equal(x[:, 9:], want[1])

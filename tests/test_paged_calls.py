@@ -146,3 +146,47 @@ def test_sketch_matrices_of_other_heads_are_refused():
         setattr(tabs, k, getattr(tabs, k)[:2])
         with pytest.raises(ValueError, match="tables"):
             api.encode(lay, tabs, torch.zeros(4, 4, 64), api.Cache.empty(lay, 4, 16, device="cpu"))
+
+
+def test_rope_outputs_over_the_other_tensor_are_refused():
+    """Both tensors turn in one launch: an output over the other's input, or over the other output, would race."""
+    t, p = paged.RopeTable((16,), device="cpu"), torch.zeros(1, 4, dtype=torch.int32)
+    buf = torch.zeros(4, 8, 32)
+    a, b, c = buf[:, :2], buf[:, 2:4], buf[:, 4:6]
+    for kw, match in ((dict(out=b), "overlap"), (dict(k_out=a), "overlap"), (dict(out=b, k_out=a), "overlap"),
+                      (dict(out=c, k_out=c), "overlap"), (dict(out=c, k_out=buf[:, 5:7]), "overlap"),
+                      (dict(out=buf[:, 1:3]), "overlap"),
+                      (dict(out=a, k_out=b), "CUDA"), (dict(out=c, k_out=buf[:, 6:]), "CUDA"), (dict(out=c), "CUDA"),
+                      (dict(), "CUDA")):
+        with pytest.raises(ValueError, match=match):
+            paged.rope(a, p, t, k=b, **kw)
+    one = torch.zeros(4, 1, 32)
+    with pytest.raises(ValueError, match="overlap"):
+        paged.rope(buf[:, :2], p, t, out=buf.view(-1)[32:288].view(4, 2, 32))  # other strides over the same rows
+    with pytest.raises(ValueError, match="CUDA"):
+        paged.rope(one, p, t, k=one.clone(), out=one)
+    with pytest.raises(ValueError, match="CUDA"):
+        paged.rope(a, p, t, k=a)  # one input given twice is only read
+
+
+def test_views_that_may_share_memory():
+    """Views called apart share no element; and those of a fused buffer, by heads or between them, are called apart."""
+    rng = np.random.default_rng(3)
+    buf = torch.zeros(4000)
+    apart = 0
+    for _ in range(3000):
+        v = []
+        for _ in range(2):
+            n, h, d = (int(rng.integers(1, k)) for k in (5, 4, 9))
+            sh = int(rng.integers(d, 3 * d + 1))
+            s = int(rng.integers(1, 4)) * sh * int(rng.integers(1, 5))
+            v.append(buf.as_strided((n, h, d), (s, sh, 1), int(rng.integers(0, 200))))
+        cells = [set((t.storage_offset() + np.add.outer(np.add.outer(np.arange(t.shape[0]) * t.stride(0),
+                      np.arange(t.shape[1]) * t.stride(1)), np.arange(t.shape[2]))).ravel().tolist()) for t in v]
+        if not paged._meet(*v):
+            apart += 1
+            assert not cells[0] & cells[1], [(t.shape, t.stride(), t.storage_offset()) for t in v]
+    assert apart > 300
+    x = torch.zeros(5, 12, 16)
+    for a, b in ((x[:, :8], x[:, 8:]), (x[:, 0::2], x[:, 1::2]), (x[..., :8], x[..., 8:]), (x[:1, :8], x[:1, 8:]), (x[:2], x[2:])):
+        assert not paged._meet(a, b) and not paged._meet(b, a) and paged._meet(a, a)
