@@ -220,6 +220,8 @@ class PagedCache:
             raise ValueError("page_size must be a positive multiple of 16, with at least one page and head")
         if self.status is None:
             self.status = torch.zeros(1, dtype=torch.int32, device=p.device)
+        elif self.status.dtype != torch.int32 or self.status.numel() != 1:
+            raise ValueError(f"status must be int32 [1], got {self.status.dtype} {tuple(self.status.shape)}")
         if any(t is not None and t.device != p.device for t in (g, v, self.status)):
             raise ValueError("the cache's tensors must be on one device")
         self.shape = (n, h, p.shape[2], s, None if v is None else v.shape[3])  # pages, heads, words, page size, d

@@ -190,3 +190,13 @@ def test_views_that_may_share_memory():
     x = torch.zeros(5, 12, 16)
     for a, b in ((x[:, :8], x[:, 8:]), (x[:, 0::2], x[:, 1::2]), (x[..., :8], x[..., 8:]), (x[:1, :8], x[:1, 8:]), (x[:2], x[2:])):
         assert not paged._meet(a, b) and not paged._meet(b, a) and paged._meet(a, a)
+
+
+def test_a_status_word_is_one_int32():
+    lay, _, c = _cpu()
+    for s in (torch.zeros(0, dtype=torch.int32), torch.zeros(1), torch.zeros(1, dtype=torch.int64), torch.zeros(4, dtype=torch.uint8),
+              torch.zeros((), dtype=torch.int16)):
+        with pytest.raises(ValueError, match="status"):
+            paged.PagedCache(c.packed, c.gamma, c.V, s)
+    for s in (torch.zeros(1, dtype=torch.int32), torch.zeros((), dtype=torch.int32)):
+        assert paged.PagedCache(c.packed, c.gamma, c.V, s).status is s
