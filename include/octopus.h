@@ -333,7 +333,7 @@ typedef struct octo_page_table {
   const int32_t* pages; /* device [n_seqs][stride]; entries behind a sequence's last page are not read */
   int64_t stride;       /* entries between rows, >= max_pages */
   int32_t n_seqs;
-  int32_t max_pages;    /* entries per row that may be read */
+  int32_t max_pages;    /* entries per row that may be read; max_pages * page_size at most 2^31 - 1 - 65536 */
 } octo_page_table;
 
 enum octo_paged_status {

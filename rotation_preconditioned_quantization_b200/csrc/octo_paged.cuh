@@ -41,8 +41,8 @@ inline int check_pages(const octo_pages* p) {
 inline int check_table(const octo_page_table* t, int page_size) {
   if (!t || t->n_seqs < 0 || t->max_pages < 0 || t->stride < t->max_pages) return OCTO_EINVAL;
   if (t->n_seqs > 0 && t->max_pages > 0 && !t->pages) return OCTO_EINVAL;
-  // slots are 32-bit
-  if (static_cast<int64_t>(t->max_pages) * page_size > (INT32_MAX - 1024)) return OCTO_EUNSUPPORTED;
+  // slots are 32-bit, also rounded up to the tiles and clusters that share them (eviction: 4096 slots)
+  if (static_cast<int64_t>(t->max_pages) * page_size > INT32_MAX - 65536) return OCTO_EUNSUPPORTED;
   return OCTO_OK;
 }
 

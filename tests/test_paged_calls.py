@@ -200,3 +200,15 @@ def test_a_status_word_is_one_int32():
             paged.PagedCache(c.packed, c.gamma, c.V, s)
     for s in (torch.zeros(1, dtype=torch.int32), torch.zeros((), dtype=torch.int32)):
         assert paged.PagedCache(c.packed, c.gamma, c.V, s).status is s
+
+
+@pytest.mark.parametrize("page,slots,want", [(16, 2 ** 31 - 1 - 1024 - 15, EUNS), (16, 2 ** 31 - 65536, EUNS), (16, 2 ** 31 - 65552, OK),
+                                             (1 << 20, 2 ** 31 - (1 << 20), OK)])
+def test_slots_leave_room_for_rounded_up_tiles(page, slots, want):
+    """Slot numbers are 32-bit, and the kernels round them up to the tiles and clusters that share them."""
+    n = slots // page
+    lay, pages, table = api.Layout(64, 2), _lib.OctoPages(256, 256, 256, 4, 2, page, None), _lib.OctoPageTable(256, n, 0, n)
+    p, t = ctypes.byref(pages), ctypes.byref(table)
+    lib = _lib.lib()
+    assert lib.octo_paged_write(lay.ref, p, t, 256, 256, 8, 256, 128, 64, 4, 256, 256, None) == want
+    assert lib.octo_paged_evict(lay.ref, p, t, 256, 256, 64, 16, 0, 0, p, t, 256, 256, None, None) == want
