@@ -363,7 +363,8 @@ __global__ void __launch_bounds__(256) paged_gather_kernel(const __grid_constant
   const int i = blockIdx.y / a.src.n_heads, h = blockIdx.y % a.src.n_heads, P = a.src.page_size;
   const int k0 = blockIdx.x * TILE, nt = min(TILE, a.keep - k0);
   if (blockIdx.x == 0 && h == 0 && threadIdx.x == 0)
-    a.new_lens[i] = min(min(max(static_cast<int>(load_now(a.seq_lens + i)), 0), a.cap), a.keep);
+    // (a plain load: new_lens may be seq_lens, and the read-only path is for memory that the kernel does not write)
+    a.new_lens[i] = min(min(max(*const_cast<const volatile int32_t*>(a.seq_lens + i), 0), a.cap), a.keep);
   for (int t = threadIdx.x; t < nt; t += 256) {
     const int slot = __ldg(a.kept + static_cast<int64_t>(blockIdx.y) * a.keep + k0 + t);
     int64_t from = kNone, to = kNone, row = kNone, page = 0;

@@ -212,3 +212,10 @@ def test_slots_leave_room_for_rounded_up_tiles(page, slots, want):
     lib = _lib.lib()
     assert lib.octo_paged_write(lay.ref, p, t, 256, 256, 8, 256, 128, 64, 4, 256, 256, None) == want
     assert lib.octo_paged_evict(lay.ref, p, t, 256, 256, 64, 16, 0, 0, p, t, 256, 256, None, None) == want
+
+
+def test_lengths_that_may_be_replaced_in_place_are_not_read_as_read_only():
+    """new_lens may be seq_lens: the launch that writes the one must not read the other through the read-only path."""
+    text = open(os.path.join(os.path.dirname(paged.__file__), "csrc", "octo_paged_move.cu")).read()
+    body = text[text.index("paged_gather_kernel("):]
+    assert not re.search(r"(load_now|__ldg)\(a\.seq_lens", body[:body.index("\n}\n")])
