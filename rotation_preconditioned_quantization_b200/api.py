@@ -246,9 +246,15 @@ def decode_attn_workspace_bytes(layout: Layout, B: int, Hq: int, Hkv: int, Lq: i
 class Workspace:
     """Device workspace for decode_attn: status word, ticket counters (zeroed
     here, left zero by every completed call) and split partials. The paged
-    calls, whose scratch lies behind status and counters, take one as well."""
+    calls, whose scratch lies behind status and counters, take one as well.
+    Size it before a capture: what is made within one is zeroed when the graph
+    runs, and not before."""
 
     def __init__(self, nbytes: int, device="cuda"):
+        self._captured, self._replaced = False, []
+        self._allocate(nbytes, device)
+
+    def _allocate(self, nbytes: int, device):
         n = max(512, (int(nbytes) + 255) // 256 * 256)
         self.buf = torch.zeros(n // 4, dtype=torch.int32, device=device)
 
@@ -264,8 +270,15 @@ class Workspace:
         return self.buf[64:64 + n_heads]
 
     def ensure(self, nbytes: int):
+        """At least nbytes, for a call about to be made. A buffer that a captured call holds lives as long as the
+        workspace: its graph may be replayed after a larger call has replaced it."""
         if nbytes > self.nbytes:
-            self.__init__(nbytes, self.buf.device)
+            if self._captured:
+                self._replaced.append(self.buf)
+                self._captured = False
+            self._allocate(nbytes, self.buf.device)
+        if self.buf.is_cuda and torch.cuda.is_current_stream_capturing():
+            self._captured = True
         return self
 
 

@@ -415,9 +415,7 @@ def _scratch(workspace, need: int, cache: PagedCache):
         return torch.empty((need + 255) // 256 * 64, dtype=_I32, device=cache.packed.device)
     if workspace.buf.get_device() != cache.index:
         raise ValueError(f"the workspace is on {workspace.buf.device}, the cache on {cache.packed.device}")
-    if need > workspace.buf.numel() * 4:
-        workspace.ensure(need)
-    return workspace.buf
+    return workspace.ensure(need).buf
 
 
 @_on_its_stream

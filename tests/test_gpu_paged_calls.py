@@ -212,3 +212,33 @@ def test_rope_into_another_part_of_a_fused_buffer(cuda_ok, dtype):
     want = paged.rope(x[:, :4].clone(), pos, table, k=x[:, 4:5].clone())
     paged.rope(x[:, :4], pos, table, k=x[:, 4:5], out=x[:, 5:9], k_out=x[:, 9:])
     assert torch.equal(x[:, 5:9], want[0]) and torch.equal(x[:, 9:], want[1])
+
+
+def test_a_workspace_that_grows_keeps_what_a_graph_holds(cuda_ok):
+    """A captured call's scratch stays its own when a later call needs more than the workspace has."""
+    pool = pr.Pool(101, 64, 2, 16, 2, [300])
+    q, big = _queries(102, 4, 4, 64), _queries(103, 4000, 4, 64)
+    lse, blse = torch.full((4, 4), 5.0, device="cuda"), torch.full((4000, 4), 5.0, device="cuda")
+    m = torch.rand(1, 2, 300, device="cuda")
+    ws = api.Workspace(paged.paged_mass_workspace_bytes(pool.lay, 4, 1, 4, 2))
+    out = torch.empty_like(m)
+    mass = lambda q, lse, out: paged.paged_mass(pool.lay, pool.tables, q, lse, pool.cache, pool.page_table, pool.seq_lens,  # noqa: E731
+                                                m, out=out, workspace=ws)
+    cu = _i32([0, 4])
+    call = lambda out: paged.paged_mass(pool.lay, pool.tables, q, lse, pool.cache, pool.page_table, pool.seq_lens, m, cu_q=cu,  # noqa: E731
+                                        out=out, workspace=ws)
+    want = call(torch.empty_like(m))
+    torch.cuda.synchronize()
+    size = ws.nbytes
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(out)
+    mass(big, blse, torch.empty_like(m))
+    assert ws.nbytes > size
+    others = [torch.full((size // 4,), 7, dtype=torch.int32, device="cuda") for _ in range(8)]  # what took freed memory
+    for _ in range(2):
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    assert all(x.eq(7).all() for x in others)

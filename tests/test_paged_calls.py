@@ -219,3 +219,17 @@ def test_lengths_that_may_be_replaced_in_place_are_not_read_as_read_only():
     text = open(os.path.join(os.path.dirname(paged.__file__), "csrc", "octo_paged_move.cu")).read()
     body = text[text.index("paged_gather_kernel("):]
     assert not re.search(r"(load_now|__ldg)\(a\.seq_lens", body[:body.index("\n}\n")])
+
+
+def test_a_workspace_keeps_the_buffers_that_captured_calls_hold():
+    ws = api.Workspace(1 << 12, device="cpu")
+    first = ws.buf
+    ws.ensure(1 << 13)
+    assert ws.nbytes == 1 << 13 and not ws._replaced  # no call was captured: nothing is kept
+    ws._captured = True
+    held = ws.buf
+    assert ws.ensure(1 << 12) is ws and ws.buf is held
+    ws.ensure(1 << 14)
+    assert ws._replaced == [held] and ws.buf is not held and ws.buf is not first and ws.nbytes == 1 << 14
+    ws.ensure(1 << 15)
+    assert ws._replaced == [held]
