@@ -46,6 +46,18 @@ inline int check_table(const octo_page_table* t, int page_size) {
   return OCTO_OK;
 }
 
+// SMs of the current device.
+inline int sm_count() {
+  static std::atomic<int> known[kLaunchCacheDevices];
+  int dev = 0, sms = 148;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+  const bool cached = dev >= 0 && dev < kLaunchCacheDevices;
+  if (cached && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 148;
+  if (cached) known[dev].store(sms, std::memory_order_relaxed);
+  return sms;
+}
+
 // The paged calls' scratch starts behind what octo_decode_attn keeps at the
 // front of a workspace from one call to the next: a status word, and at byte
 // 256 an arrival counter per cache head, at most 65535.
@@ -107,6 +119,16 @@ __device__ __forceinline__ Seq seq_of(const Table& t, const int32_t* seq_lens, c
   s.len = min(max(n, 0), cap);
   if (tell && (s.row0 != a || s.fresh != z - a || s.len != n)) report(t.status, OCTO_PAGED_BAD_LENGTH);
   return s;
+}
+
+// Sums over the lanes up to this one.
+__device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
 }
 
 // A load that starts here: the compiler neither moves it to its use nor the

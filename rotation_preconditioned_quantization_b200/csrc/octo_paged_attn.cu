@@ -114,14 +114,6 @@ struct Place {
   int64_t start, count, total;  // the piece's first key tile in the list and their number; tiles of the list
   int i, h, m, tile;
 };
-__device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += u;
-  }
-  return v;
-}
 __device__ int64_t total_tiles(const AttnArgs& a, int lane, bool tell) {
   int64_t n = 0;
   for (int i = lane; i < a.t.n_seqs; i += 32)
@@ -1197,17 +1189,6 @@ __global__ void __launch_bounds__(256) paged_attn_join(const __grid_constant__ A
 }
 
 // ---- host -------------------------------------------------------------------
-static int sm_count() {
-  static std::atomic<int> known[kLaunchCacheDevices];
-  int dev = 0, sms = 148;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 148;
-  const bool cached = dev >= 0 && dev < kLaunchCacheDevices;
-  if (cached && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
-  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 148;
-  if (cached) known[dev].store(sms, std::memory_order_relaxed);
-  return sms;
-}
-
 static int attn_ctas() { return std::min(sm_count(), kJoin); }
 
 static bool encode_v_map(CUtensorMap* m, const octo_pages* p, int D, int box) {

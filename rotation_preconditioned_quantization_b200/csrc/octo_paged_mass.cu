@@ -73,15 +73,6 @@ __device__ __forceinline__ void split2(float x, float y, float grid, uint32_t& h
 
 __device__ __forceinline__ int query_tiles(const Seq& s, int g) { return (s.fresh * g + kQRows - 1) / kQRows; }
 
-__device__ __forceinline__ int64_t scan64(int64_t v, int lane) {
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += u;
-  }
-  return v;
-}
-
 // ---- queries: rotate, scale, split ---------------------------------------------
 template <int D>
 __global__ void __launch_bounds__(256) paged_mass_prep(const __grid_constant__ MassArgs a) {
@@ -94,7 +85,7 @@ __global__ void __launch_bounds__(256) paged_mass_prep(const __grid_constant__ M
     for (int base = 0; base < a.t.n_seqs; base += 32) {
       const int i = base + lane;
       const int mt = i < a.t.n_seqs ? query_tiles(seq_of(a.t, a.seq_lens, a.cu, a.n_rows, i, blockIdx.x == 0 && h == 0), a.g) : 0;
-      const int64_t end = before + scan64(mt, lane);
+      const int64_t end = before + warp_scan(mt, lane);
       if (static_cast<int64_t>(blockIdx.x) < end && static_cast<int64_t>(blockIdx.x) >= end - mt) {
         s_i = i;
         s_m = static_cast<int>(blockIdx.x - (end - mt));
@@ -234,8 +225,8 @@ __device__ UnitPlace find_units(const MassArgs& a, int lane) {
     Seq s{0, 0, 0};
     if (i < a.t.n_seqs) s = seq_of(a.t, a.seq_lens, a.cu, a.n_rows, i);
     const int64_t n = static_cast<int64_t>(units_of(s)) * a.t.n_heads, c = unit_cost(s, a.g), w = n * c;
-    const int64_t end = before + scan64(w, lane), start = end - w;
-    const int64_t tend = tiles + scan64(query_tiles(s, a.g), lane);
+    const int64_t end = before + warp_scan(w, lane), start = end - w;
+    const int64_t tend = tiles + warp_scan(query_tiles(s, a.g), lane);
     // units k of this sequence with start + k * c in [w0, w1)
     const int64_t k0 = min(n, max(static_cast<int64_t>(0), (w0 - start + c - 1) / c)),
                   k1 = min(n, max(static_cast<int64_t>(0), (w1 - start + c - 1) / c));
@@ -614,17 +605,6 @@ __global__ void __launch_bounds__(576, 1) paged_mass_kernel(const __grid_constan
 }
 
 // ---- host -------------------------------------------------------------------------
-static int mass_sms() {
-  static std::atomic<int> known[kLaunchCacheDevices];
-  int dev = 0, sms = 148;
-  if (cudaGetDevice(&dev) != cudaSuccess) return 148;
-  const bool cached = dev >= 0 && dev < kLaunchCacheDevices;
-  if (cached && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
-  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 148;
-  if (cached) known[dev].store(sms, std::memory_order_relaxed);
-  return sms;
-}
-
 // row tiles of all sequences, at most
 static int64_t most_tiles(int64_t n_rows, int n_seqs, int g) { return n_rows * g / kQRows + n_seqs; }
 
@@ -638,7 +618,7 @@ static cudaError_t launch_mass(const MassArgs& a, cudaStream_t st) {
   int resident = 0;
   e = launch_setup(paged_mass_kernel<D, B>, cache, MassCfg<D, B>::THREADS, MassCfg<D, B>::SMEM, resident);
   if (e != cudaSuccess) return e;
-  paged_mass_kernel<D, B><<<mass_sms(), MassCfg<D, B>::THREADS, MassCfg<D, B>::SMEM, st>>>(a);
+  paged_mass_kernel<D, B><<<sm_count(), MassCfg<D, B>::THREADS, MassCfg<D, B>::SMEM, st>>>(a);
   return cudaGetLastError();
 }
 
