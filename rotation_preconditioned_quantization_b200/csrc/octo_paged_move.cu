@@ -152,8 +152,7 @@ __device__ __forceinline__ uint32_t order_bits(float v) {
 }
 
 // C blocks (a cluster) share a (sequence, head): its passes are bound by one
-// SM's instructions (32768 slots took one block 42 us), and few heads would
-// leave the other SMs idle. A warp owns a contiguous run of slots, lanes along
+// SM's instructions, and few heads would leave the other SMs idle. A warp owns a contiguous run of slots, lanes along
 // it. HELD: the slots' ordered bits are kept in shared memory; else every pass
 // reads the masses again.
 template <bool HELD, int C>
@@ -460,9 +459,12 @@ extern "C" int octo_paged_evict(const octo_layout* L, const octo_pages* src, con
   s.new_mass = new_mass;
   s.status = src->status;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // one block up to 4096 slots (11.7 us in all at 1500), four from there (32768: 42 -> 26 us), and from what they can
-  // hold the masses are read in every pass
-  if ((s.cap <= 4096 ? launch_select<true, 1>(s, rows, st)
+  // One block or a cluster of four per (sequence, head). Four share the slots but meet eight times, and every block fills
+  // an SM: they pay for long rows, and only while all clusters run at once. One / four, both launches of a call in us:
+  // 32 rows of 4096 slots 13.0 / 21.3, of 16384 19.9 / 23.5, of 32768 29.2 / 25.5; 256 rows of 32768 54.9 / 166. Beyond
+  // what one block can hold (34976 slots) four hold them, and beyond 139904 the masses are read in every pass.
+  const bool four = s.cap > kHeld - 1024 || (s.cap > 24576 && rows <= 32);
+  if ((!four ? launch_select<true, 1>(s, rows, st)
        : s.cap <= 4 * (kHeld - 1024) ? launch_select<true, 4>(s, rows, st) : launch_select<false, 4>(s, rows, st)) != cudaSuccess)
     return OCTO_ECUDA;
   GatherArgs g{};

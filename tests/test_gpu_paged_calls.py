@@ -242,3 +242,26 @@ def test_a_workspace_that_grows_keeps_what_a_graph_holds(cuda_ok):
         torch.cuda.synchronize()
         assert torch.equal(out, want)
     assert all(x.eq(7).all() for x in others)
+
+
+@pytest.mark.parametrize("slots", [4097, 24576, 24577, 34976, 34977])
+@pytest.mark.parametrize("heads", [3, 32, 33])
+def test_evict_at_the_bounds_of_its_choice(cuda_ok, slots, heads):
+    """One block or four per head, by the slots and by how many (sequence, head) rows there are: the same slots stay."""
+    lay, keep, sink, recent = api.Layout(64, 2), 300, 5, 70
+    per = -(-slots // 256)
+    cache = paged.PagedCache.empty(lay, per + 2, heads, 256, values=False)
+    cache.gamma.copy_(torch.rand(cache.gamma.shape, generator=torch.Generator().manual_seed(1)))
+    table, dst = torch.arange(per, dtype=torch.int32, device="cuda")[None], _i32([[per, per + 1]])
+    g = torch.Generator("cuda").manual_seed(slots)
+    m = torch.rand(1, heads, slots, generator=g, device="cuda")
+    m[torch.rand(m.shape, generator=g, device="cuda") < 0.3] = 0.999  # ties at the border: the lower slots stay
+    n = slots - 1
+    lens, kept, mass = paged.paged_evict(lay, cache, table, _i32([n]), m, keep, dst, sink=sink, recent=recent)
+    cache.check()
+    w = m[0, :, :n].clone()
+    w[:, :sink], w[:, n - recent:] = 2.0, 2.0
+    want = torch.sort(w, descending=True, stable=True).indices[:, :keep].sort().values
+    assert int(lens) == keep and torch.equal(kept[0].long(), want) and torch.equal(mass[0], m[0].gather(1, want))
+    src = cache.gamma[:per].transpose(0, 1).reshape(heads, -1).gather(1, want)
+    assert torch.equal(cache.gamma[per:].transpose(0, 1).reshape(heads, -1)[:, :keep], src)
