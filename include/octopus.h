@@ -466,10 +466,10 @@ OCTO_API int octo_paged_mass(const octo_layout* L, const octo_tables* tables, co
  * pages written must not be read by this call). Two launches.
  *   mass     device fp32 [n_seqs][n_heads][mass_stride].
  *   kept     device int32 [n_seqs][n_heads][keep]: the slots kept, ascending; -1 from n on.
- *   new_lens device int32 [n_seqs]: min(n, keep); may be seq_lens.
+ *   new_lens device int32 [n_seqs]: min(n, keep); may be seq_lens itself, and must not overlap it otherwise.
  *   new_mass device fp32 [n_seqs][n_heads][keep] (0 from n on), or NULL; must not overlap mass.
  * Errors: OCTO_EINVAL (NULL pointer, keep < 1, sink or recent < 0, sink +
- * recent > keep, new_mass over mass, pools of different heads or page size, one pool with V and
+ * recent > keep, new_mass over mass, new_lens over a part of seq_lens, pools of different heads or page size, one pool with V and
  * the other without, a destination table shorter than keep), OCTO_EUNSUPPORTED (layout; n_seqs * n_heads
  * > 65535). n_seqs == 0 launches nothing. */
 OCTO_API int octo_paged_evict(const octo_layout* L, const octo_pages* src, const octo_page_table* src_table,

@@ -441,6 +441,9 @@ extern "C" int octo_paged_evict(const octo_layout* L, const octo_pages* src, con
   if (rows > 65535) return OCTO_EUNSUPPORTED;  // grid.y limit
   if (rows == 0) return OCTO_OK;
   if (!seq_lens || !mass || !kept || !new_lens) return OCTO_EINVAL;
+  const uintptr_t l0 = reinterpret_cast<uintptr_t>(seq_lens), n0 = reinterpret_cast<uintptr_t>(new_lens);
+  const uintptr_t lens_bytes = static_cast<uintptr_t>(src_table->n_seqs) * 4;
+  if (l0 != n0 && l0 < n0 + lens_bytes && n0 < l0 + lens_bytes) return OCTO_EINVAL;  // in place, or apart
   if (new_mass) {  // the choice writes it while it reads mass
     const uintptr_t m0 = reinterpret_cast<uintptr_t>(mass), o0 = reinterpret_cast<uintptr_t>(new_mass);
     if (o0 < m0 + static_cast<uintptr_t>(rows) * mass_stride * 4 && m0 < o0 + static_cast<uintptr_t>(rows) * keep * 4)

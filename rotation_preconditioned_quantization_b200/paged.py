@@ -99,7 +99,7 @@ class RopeTable:
         _lib.check(_lib.lib().octo_rope_freqs(float(theta), len(sec), sec.ctypes.data, int(bool(per_axis)), f.ctypes.data),
                    "octo_rope_freqs")
         self._theta, self._per_axis = float(theta), bool(per_axis)
-        self.c_sections = sec
+        self.c_sections, self._count = sec, len(f)
         self.freqs = torch.from_numpy(f.view(np.int64)).to(device)
         self.sections_ptr = sec.ctypes.data
 
@@ -164,10 +164,9 @@ def rope(q: torch.Tensor, positions: torch.Tensor, table: RopeTable, k: torch.Te
     if dt is None or q.dim() != 3:
         raise ValueError(f"q must be float32 or bfloat16 [tokens][heads][d], got {q.dtype} {tuple(q.shape)}")
     n, _, d = q.shape
-    axes, freqs = len(table.sections), table.freqs
-    if freqs.dtype is not torch.int64 or freqs.numel() < sum(table.sections) or not freqs.is_contiguous():
-        raise ValueError(f"the table's freqs must be contiguous int64 [{sum(table.sections)}], got {freqs.dtype} "
-                         f"{tuple(freqs.shape)}")
+    axes, freqs = len(table._sections), table.freqs
+    if freqs.dtype is not torch.int64 or freqs.numel() < table._count or not freqs.is_contiguous():
+        raise ValueError(f"the table's freqs must be contiguous int64 [{table._count}], got {freqs.dtype} {tuple(freqs.shape)}")
     if positions.dtype is not _I32 or positions.shape != (axes, n) or (n > 1 and positions.stride(1) != 1):
         raise ValueError(f"positions must be int32 [{axes}][{n}], contiguous in its last dimension, got "
                          f"{positions.dtype} {tuple(positions.shape)}")
@@ -536,6 +535,8 @@ def paged_evict(layout: api.Layout, cache: PagedCache, page_table: torch.Tensor,
         new_lens = torch.empty((B,), dtype=_I32, device=dev)
     else:
         _vector(new_lens, "new_lens", B)
+        if new_lens.data_ptr() != seq_lens.data_ptr() and abs(new_lens.data_ptr() - seq_lens.data_ptr()) < 4 * B:
+            raise ValueError("new_lens must be seq_lens itself or not overlap it")
     if new_mass is None:
         new_mass = torch.empty((B, H, keep), dtype=_F32, device=dev)
     else:

@@ -233,3 +233,19 @@ def test_a_workspace_keeps_the_buffers_that_captured_calls_hold():
     assert ws._replaced == [held] and ws.buf is not held and ws.buf is not first and ws.nbytes == 1 << 14
     ws.ensure(1 << 15)
     assert ws._replaced == [held]
+
+
+def test_new_lengths_over_a_part_of_the_old_are_refused():
+    lay, _, c = _cpu()
+    buf, table = torch.tensor([5, 6, 7], dtype=torch.int32), _i32([[0, 1], [2, 3]])
+    ev = lambda a, b: paged.paged_evict(lay, c, table, a, torch.zeros(2, 2, 32), 16, table, new_lens=b)  # noqa: E731
+    for a, b in ((buf[:2], buf[1:]), (buf[1:], buf[:2])):
+        with pytest.raises(ValueError, match="overlap"):
+            ev(a, b)
+    for a, b in ((buf[:2], buf[:2]), (buf[:2], buf[:2].clone())):
+        with pytest.raises(ValueError, match="CUDA"):
+            ev(a, b)
+    pages, tab = _lib.OctoPages(256, 256, 256, 4, 2, 16, None), _lib.OctoPageTable(256, 4, 2, 4)
+    for lens, new in ((256, 260), (260, 256)):
+        assert _lib.lib().octo_paged_evict(lay.ref, ctypes.byref(pages), ctypes.byref(tab), lens, 512, 64, 16, 0, 0,
+                                           ctypes.byref(pages), ctypes.byref(tab), 1024, new, None, None) == EINVAL
