@@ -351,8 +351,8 @@ enum octo_paged_status {
  * sections[1] to axis 1, and so on. e_i = i / F with one frequency scale over
  * all axes, or j / sections[axis] for the j-th frequency of its axis
  * (per_axis). inverse turns back: it is the transpose, so also the gradient
- * of the forward call. Angles are exact to 2^-32 of a turn at every 32-bit
- * position.
+ * of the forward call. Angles are formed to 2^-32 of a turn at every 32-bit
+ * position and rounded to fp32 for their cosine and sine: 2^-26 of a turn.
  *   x0, y0  device rows [n_tokens][heads0][d] in and out, dtype OCTO_F32 or
  *           OCTO_BF16, element strides (token, head), the last axis
  *           contiguous; y may be x, and must not overlap it otherwise, nor the
@@ -419,7 +419,9 @@ OCTO_API int octo_paged_write(const octo_layout* L, const octo_pages* pages, con
  * Keys and queries enter the tensor cores as fp16 (queries scaled by a power
  * of two per row), weights and V as bf16; sums and softmax statistics are
  * fp32 (out is divided by the sum of the rounded weights, lse is that of the
- * unrounded ones). Values of slots that a row does not see, but another row of its
+ * unrounded ones). An fp32 out therefore carries no more than these types do,
+ * errors of about 1e-3 relative; octo_decode_attn keeps about 16 bits of
+ * both. Rows of no sequence are left as they were. Values of slots that a row does not see, but another row of its
  * sequence does, must be finite, and the magnitudes of a sequence's values sum
  * to less than 2^60 per coordinate. Two launches.
  * Supported: d in {64, 128}, b in {2, 3, 4}, Hq / n_heads <= 256.

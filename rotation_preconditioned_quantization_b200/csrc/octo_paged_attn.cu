@@ -37,8 +37,8 @@
 //
 // Bound by the softmax warps, which read S twice from tensor memory (a bound
 // on the logits, then the weights) in turn with the products: 512 tokens of
-// 32/8 heads over 32768 slots (d = 128, b = 3) take 369 us, 750 TFLOP/s;
-// 1024 tokens of 16 heads over 65536 slots (d = 64, b = 2) 585 us. With few
+// 32/8 heads over 32768 slots (d = 128, b = 3) take 370 us, 750 TFLOP/s;
+// 1024 tokens of 16 heads over 65536 slots (d = 64, b = 2) 588 us. With few
 // rows the decode of key tiles bounds: one token over 32767 slots takes 52 us
 // for 83 MB.
 

@@ -25,7 +25,7 @@
 // the weights of the unit's first and second 128 slots, 8-11 and 12-15 decode
 // them, 16 issues the products, 17 copies query tiles. Both halves use a
 // query tile while it is in shared memory, which halves what the copies move.
-// 512 tokens of 32/8 heads over 16384 slots (d = 128, b = 3) take 282 us, 130
+// 512 tokens of 32/8 heads over 16384 slots (d = 128, b = 3) take 286 us, 130
 // of them the products at full rate; single tokens of four sequences of up to
 // 32767 slots, bound by the decode, 63 us.
 

@@ -6,8 +6,9 @@
 // their places once, then copies plane by plane (lanes along tokens, so that
 // a page's part of a plane is one contiguous access) and V in 16-byte pieces.
 // Writing up to 2047 tokens of four sequences (8 heads, d = 128, b = 4; 22 MB)
-// takes 9.4 us, one token of 64 sequences 4.6 us; cutting 32 heads from 32768
-// to 8192 slots 64 us, 26 of them the choice.
+// takes 9.4 us (1024 blocks, where 592 are resident: a wave and most of another),
+// one token of 64 sequences 4.6 us; cutting 32 heads from 32768 to 8192 slots
+// 65 us, 25 of them the choice.
 //
 // Which tokens an eviction keeps: per (sequence, head) a block finds the
 // rank-th largest mass of the middle slots by three histogram passes over the

@@ -430,6 +430,9 @@ def paged_attn(layout: api.Layout, tables: api.DeviceTables, q: torch.Tensor, ca
     (``dtype`` float32 or bfloat16, by default q's), and with ``lse`` (True, or a float32 [rows][Hq] tensor) the pair
     (out, lse) with lse = ln sum exp(scale * logits).
 
+    Queries enter the tensor cores as one fp16 value each, weights as bf16: a float32 output carries no more than that
+    (errors of about 1e-3 relative). Rows of no sequence are left as they were (an ``out`` made here: uninitialised).
+
     A workspace serves one call at a time, whichever (``decode_attn``'s too): calls that may overlap on the GPU (streams,
     graphs) need one each. None allocates it for this call.
     """
