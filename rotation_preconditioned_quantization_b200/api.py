@@ -273,6 +273,8 @@ class Workspace:
         """At least nbytes, for a call about to be made. A buffer that a captured call holds lives as long as the
         workspace: its graph may be replayed after a larger call has replaced it."""
         if nbytes > self.nbytes:
+            if self.buf.is_cuda:  # earlier calls may still run, on another stream than the one that made the buffer
+                self.buf.record_stream(torch.cuda.current_stream(self.buf.device))
             if self._captured:
                 self._replaced.append(self.buf)
                 self._captured = False

@@ -265,3 +265,29 @@ def test_evict_at_the_bounds_of_its_choice(cuda_ok, slots, heads):
     assert int(lens) == keep and torch.equal(kept[0].long(), want) and torch.equal(mass[0], m[0].gather(1, want))
     src = cache.gamma[:per].transpose(0, 1).reshape(heads, -1).gather(1, want)
     assert torch.equal(cache.gamma[per:].transpose(0, 1).reshape(heads, -1)[:, :keep], src)
+
+
+def test_a_workspace_that_grows_behind_a_call_that_still_runs(cuda_ok):
+    """Calls in order on a side stream, the second larger: the buffer that it replaces, made on the current stream, goes to
+    nobody before the first call is done."""
+    pool = pr.Pool(104, 64, 2, 16, 2, [300])
+    q, big = _queries(105, 4, 4, 64), _queries(106, 4000, 4, 64)
+    lse, blse = torch.full((4, 4), 5.0, device="cuda"), torch.full((4000, 4), 5.0, device="cuda")
+    m = torch.rand(1, 2, 300, device="cuda")
+    mass = lambda q, lse, out, **kw: paged.paged_mass(pool.lay, pool.tables, q, lse, pool.cache, pool.page_table, pool.seq_lens,  # noqa: E731
+                                                      m, cu_q=_i32([0, len(q)]) if not kw else kw.pop("cu"), out=out, **kw)
+    want = mass(q, lse, torch.empty_like(m)), mass(big, blse, torch.empty_like(m))
+    outs, cus = [torch.empty_like(m) for _ in range(2)], [_i32([0, 4]), _i32([0, 4000])]
+    ws = api.Workspace(paged.paged_mass_workspace_bytes(pool.lay, 4, 1, 4, 2))
+    size, side = ws.nbytes, torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(40_000_000)  # some twenty milliseconds
+    mass(q, lse, outs[0], cu=cus[0], workspace=ws, stream=side)
+    mass(big, blse, outs[1], cu=cus[1], workspace=ws, stream=side)
+    assert ws.nbytes > size
+    others = [torch.full((size // 4,), 7, dtype=torch.int32, device="cuda") for _ in range(8)]  # what takes freed memory
+    torch.cuda.synchronize()
+    assert all(x.eq(7).all() for x in others)
+    assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
+    pool.cache.check()
