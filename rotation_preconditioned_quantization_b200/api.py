@@ -17,6 +17,8 @@ the codec runs in the library's CUDA kernels (``octo_encode``,
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import math
 from dataclasses import dataclass, field
 
@@ -29,9 +31,38 @@ ROUND_SCALAR = _lib.ROUND_SCALAR
 ROUND_JOINT = _lib.ROUND_JOINT
 
 
-def _stream_ptr(stream=None) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return int(s.cuda_stream)
+# the current device and stream without the public functions' start-up checks: these calls are a few microseconds of GPU
+# work, and the checks would take longer
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _on(index: int, stream, call):
+    """call(stream handle) with the tensors' device current, on ``stream`` or torch's current stream there."""
+    if index < 0:
+        raise ValueError("the tensors must be on a CUDA device")
+    if stream is not None and stream.device_index != index:
+        raise ValueError(f"the stream is on device {stream.device_index}, the tensors on device {index}")
+    if index == _current_device():
+        return call(_raw_stream(index) if stream is None else stream.cuda_stream)
+    with torch.cuda.device(index):
+        return call(_raw_stream(index) if stream is None else stream.cuda_stream)
+
+
+def _on_its_stream(f):
+    """With ``stream``, by keyword or by position, f runs with it current: what f allocates or fills belongs to the stream
+    that uses it."""
+    at = list(inspect.signature(f).parameters).index("stream")
+
+    @functools.wraps(f)
+    def call(*args, **kw):
+        stream = args[at] if len(args) > at else kw.get("stream")
+        if stream is None:
+            return f(*args, **kw)
+        with torch.cuda.stream(stream):
+            return f(*args, **kw)
+    return call
 
 
 def _ptr(t) -> int | None:
@@ -205,14 +236,15 @@ def encode(layout: Layout, tables: DeviceTables, keys: torch.Tensor, cache: Cach
     _check_cache(layout, tables, cache, n_heads, keys)
     if tables.dir_t.numel() < layout.n_dir - 1 or tables.rho_t.numel() < layout.n_rho - 1:
         raise ValueError(f"the tables hold {tables.dir_t.numel()} and {tables.rho_t.numel()} thresholds: they are not of {layout!r}")
-    st = _lib.lib().octo_encode(layout.ref, tables.ref, _ptr(keys), dt, n_heads, n_tok, keys.stride(0), keys.stride(1),
-                                cache.cap, off, _ptr(cache.packed), _ptr(cache.gamma), _ptr(cache.qjl_bits),
-                                _ptr(cache.qjl_norm), _stream_ptr(stream))
+    st = _on(cache.gamma.get_device(), stream, lambda s: _lib.lib().octo_encode(
+        layout.ref, tables.ref, _ptr(keys), dt, n_heads, n_tok, keys.stride(0), keys.stride(1), cache.cap, off,
+        _ptr(cache.packed), _ptr(cache.gamma), _ptr(cache.qjl_bits), _ptr(cache.qjl_norm), s))
     _lib.check(st, "octo_encode")
     cache.length = max(cache.length, off + n_tok)
     return cache
 
 
+@_on_its_stream
 def dequant(layout: Layout, tables: DeviceTables, cache: Cache, n_tokens: int | None = None, token_offset: int = 0,
             n_heads: int | None = None, dtype=torch.float32, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Reconstructed keys k_hat = gamma R^T u_hat of tokens [token_offset, token_offset + n_tokens)
@@ -233,8 +265,8 @@ def dequant(layout: Layout, tables: DeviceTables, cache: Cache, n_tokens: int | 
     elif tuple(out.shape) != shape or not out.is_contiguous():
         raise ValueError(f"out must be a contiguous {shape} tensor")
     _check_cache(layout, tables, cache, h, out)
-    st = _lib.lib().octo_dequant(layout.ref, tables.ref, h, n, cache.cap, int(token_offset), _ptr(cache.packed),
-                                 _ptr(cache.gamma), _ptr(out), dt, _stream_ptr(stream))
+    st = _on(cache.gamma.get_device(), stream, lambda s: _lib.lib().octo_dequant(
+        layout.ref, tables.ref, h, n, cache.cap, int(token_offset), _ptr(cache.packed), _ptr(cache.gamma), _ptr(out), dt, s))
     _lib.check(st, "octo_dequant")
     return out
 
@@ -284,6 +316,7 @@ class Workspace:
         return self
 
 
+@_on_its_stream
 def decode_attn(layout: Layout, tables: DeviceTables, q: torch.Tensor, cache: Cache, V: torch.Tensor | None,
                 Hkv: int, kv_len: int | None = None, scale: float | None = None, out: torch.Tensor | None = None,
                 logits: torch.Tensor | None = None, workspace: Workspace | None = None, stream=None):
@@ -320,14 +353,17 @@ def decode_attn(layout: Layout, tables: DeviceTables, q: torch.Tensor, cache: Ca
                                  or not logits.is_contiguous()):
         raise ValueError(f"logits must be a contiguous float32 {(B, Hq, Lq, kv)} tensor")
     _check_cache(layout, tables, cache, B * Hkv, q, V, out, logits)
-    need = decode_attn_workspace_bytes(layout, B, Hq, Hkv, Lq, kv)
-    if workspace is None:
-        workspace = Workspace(need, q.device)
-    workspace.ensure(need)
-    ws_ptr, ws_n = _ptr(workspace.buf), workspace.nbytes
-    st = _lib.lib().octo_decode_attn(layout.ref, tables.ref, _ptr(q), qdt, B, Hq, Hkv, Lq, kv, cache.cap,
-                                     _ptr(cache.packed), _ptr(cache.gamma), _ptr(cache.qjl_bits), _ptr(cache.qjl_norm),
-                                     _ptr(V), ctypes.c_float(scale), _ptr(out), _ptr(logits), ws_ptr, ws_n,
-                                     _stream_ptr(stream))
+    if workspace is not None and workspace.buf.device != q.device:
+        raise ValueError(f"the workspace is on {workspace.buf.device}, q on {q.device}")
+
+    def call(s):
+        need = decode_attn_workspace_bytes(layout, B, Hq, Hkv, Lq, kv)
+        ws = Workspace(need, q.device) if workspace is None else workspace.ensure(need)
+        return _lib.lib().octo_decode_attn(layout.ref, tables.ref, _ptr(q), qdt, B, Hq, Hkv, Lq, kv, cache.cap,
+                                           _ptr(cache.packed), _ptr(cache.gamma), _ptr(cache.qjl_bits),
+                                           _ptr(cache.qjl_norm), _ptr(V), ctypes.c_float(scale), _ptr(out), _ptr(logits),
+                                           _ptr(ws.buf), ws.nbytes, s)
+
+    st = _on(cache.gamma.get_device(), stream, call)
     _lib.check(st, "octo_decode_attn")
     return out, logits

@@ -21,8 +21,6 @@ used on a stream other than the one they were made on need ``record_stream`` as 
 from __future__ import annotations
 
 import ctypes
-import functools
-import inspect
 import math
 from dataclasses import dataclass
 
@@ -34,38 +32,7 @@ from . import _lib, api
 _F32, _BF16, _I32 = torch.float32, torch.bfloat16, torch.int32
 _DTYPES = {_F32: _lib.F32, _BF16: _lib.BF16}
 _byref = ctypes.byref
-# the current device and stream without the public functions' start-up checks: these calls are a few microseconds of GPU
-# work, and the checks would take longer
-_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
-
-
-def _on(index: int, stream, call):
-    """call(stream handle) with the tensors' device current, on ``stream`` or torch's current stream there."""
-    if index < 0:
-        raise ValueError("the tensors must be on a CUDA device")
-    if stream is not None and stream.device_index != index:
-        raise ValueError(f"the stream is on device {stream.device_index}, the tensors on device {index}")
-    if index == _current_device():
-        return call(_raw_stream(index) if stream is None else stream.cuda_stream)
-    with torch.cuda.device(index):
-        return call(_raw_stream(index) if stream is None else stream.cuda_stream)
-
-
-def _on_its_stream(f):
-    """With ``stream``, by keyword or by position, f runs with it current: what f allocates or fills belongs to the stream
-    that uses it."""
-    at = list(inspect.signature(f).parameters).index("stream")
-
-    @functools.wraps(f)
-    def call(*args, **kw):
-        stream = args[at] if len(args) > at else kw.get("stream")
-        if stream is None:
-            return f(*args, **kw)
-        with torch.cuda.stream(stream):
-            return f(*args, **kw)
-    return call
+_on, _on_its_stream = api._on, api._on_its_stream
 
 
 def _same_device(index: int, *tensors):

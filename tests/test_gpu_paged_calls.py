@@ -291,3 +291,30 @@ def test_a_workspace_that_grows_behind_a_call_that_still_runs(cuda_ok):
     assert all(x.eq(7).all() for x in others)
     assert torch.equal(outs[0], want[0]) and torch.equal(outs[1], want[1])
     pool.cache.check()
+
+
+def test_a_decode_on_another_stream_owns_what_it_allocates(cuda_ok):
+    """Workspace (zeroed) and output of a call with ``stream``, while the current stream is busy."""
+    d, H, n = 128, 2, 20000
+    lay = api.Layout(d, 3)
+    tabs = api.DeviceTables.build(lay, 5, H)
+    g = torch.Generator("cuda").manual_seed(1)
+    cache = api.Cache.empty(lay, H, n)
+    cache.packed.random_(-2 ** 31, 2 ** 31 - 1, generator=g)
+    cache.gamma.uniform_(0.5, 2.0, generator=g)
+    cache.length = n
+    V = torch.randn(H, n, d, device="cuda", generator=g).to(torch.bfloat16)
+    q = torch.randn(1, 4 * H, 1, d, device="cuda", generator=g).to(torch.bfloat16)
+    want, keys = api.decode_attn(lay, tabs, q, cache, V, H)[0], api.dequant(lay, tabs, cache, 500)
+    side = torch.cuda.Stream()
+    junk = torch.full((1 << 22,), 7, dtype=torch.int32, device="cuda")
+    del junk
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)  # the current stream is busy for some ten milliseconds
+    out, _ = api.decode_attn(lay, tabs, q, cache, V, H, stream=side)
+    got = api.dequant(lay, tabs, cache, 500, stream=side)
+    junk = [torch.full((1 << k,), float("nan"), device="cuda") for k in range(10, 23)]
+    side.synchronize()
+    assert torch.equal(out, want) and torch.equal(got, keys)
+    torch.cuda.synchronize()
+    del junk

@@ -249,3 +249,65 @@ def test_new_lengths_over_a_part_of_the_old_are_refused():
     for lens, new in ((256, 260), (260, 256)):
         assert _lib.lib().octo_paged_evict(lay.ref, ctypes.byref(pages), ctypes.byref(tab), lens, 512, 64, 16, 0, 0,
                                            ctypes.byref(pages), ctypes.byref(tab), 1024, new, None, None) == EINVAL
+
+
+@pytest.mark.parametrize("name", ["dequant", "decode_attn"])
+def test_stream_is_current_within_the_contiguous_calls_too(name, monkeypatch):
+    """Outputs and workspaces (zeroed) that they make belong to the stream that uses them."""
+    class Entered(Exception):
+        pass
+
+    class Stream:
+        def __init__(self, s):
+            self.s = s
+
+        def __enter__(self):
+            raise Entered(self.s)
+
+        def __exit__(self, *a):
+            return False
+
+    lay, tabs, _ = _cpu()
+    flat = api.Cache.empty(lay, 2, 16, device="cpu")
+    f, args, rest = {"dequant": (api.dequant, [lay, tabs, flat], [4, 0, None, torch.float32, None]),
+                     "decode_attn": (api.decode_attn, [lay, tabs, torch.zeros(1, 4, 1, 64), flat, None, 2],
+                                     [4, None, None, True, None])}[name]
+    monkeypatch.setattr(torch.cuda, "stream", Stream)
+    side = object()
+    for a, kw in ((args, {"stream": side}), (args + rest + [side], {})):
+        with pytest.raises(Entered) as e:
+            f(*a, **kw)
+        assert e.value.args[0] is side
+    with pytest.raises(ValueError, match="CUDA"):
+        f(*args, *rest)
+
+
+def test_calls_run_on_the_tensors_device(monkeypatch):
+    """With another device current, a call is made with the tensors' one current, on its stream."""
+    now, seen = [0], []
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            now[0], self.index = self.index, now[0]
+
+        def __exit__(self, *a):
+            now[0], self.index = self.index, now[0]
+
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(api, "_current_device", lambda: now[0])
+    monkeypatch.setattr(api, "_raw_stream", lambda index: 1000 + index)
+    for index in (0, 3):
+        api._on(index, None, lambda s: seen.append((now[0], s)))
+    assert seen == [(0, 1000), (3, 1003)] and now == [0]
+    with pytest.raises(ValueError, match="CUDA"):
+        api._on(-1, None, None)
+    lay, tabs, _ = _cpu()  # and all three calls of the contiguous cache go that way
+    flat, asked = api.Cache.empty(lay, 2, 16, device="cpu"), []
+    monkeypatch.setattr(api, "_on", lambda index, stream, call: asked.append(index) or _lib.OCTO_OK)
+    api.encode(lay, tabs, torch.zeros(2, 4, 64), flat)
+    api.dequant(lay, tabs, flat)
+    api.decode_attn(lay, tabs, torch.zeros(1, 4, 1, 64), flat, None, 2, logits=True)
+    assert asked == [-1] * 3
